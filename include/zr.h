@@ -571,6 +571,139 @@ zr_status zr_step_no_alloc(const zr_plan* plan, const void* const* grad_ptrs, fl
                            float* v, void* param_out, double* d_sumsq_partials, int64_t step,
                            zr_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Matrix optimizer: orthogonalised updates ("Scaling training to thousands
+ * of GPUs", 11:24 ZeRO: optimizers such as Muon need whole tensors on one
+ * rank, which is what ZR_PARTITION_WHOLE_TENSOR is for; the pages give no
+ * formula, the rule is the published one).
+ *
+ * For an m x n matrix U and coefficients (a, b, c):
+ *   X_0 = U / (||U||_F + eps);   steps times:
+ *   A = X X^T,  X <- a X + (b A + c A A) X
+ * (for m > n the same polynomial from the right, on X^T X), which drives
+ * every singular value towards 1 and keeps the singular vectors.  Operands
+ * of the products are fp16 (scaled; X with its rounding error beside it, A
+ * and B with their diagonals in fp32), sums fp32, norms fp64; the result is
+ * within about 7e-4 of its norm of the exact iteration for 5 steps, before
+ * its own rounding to bf16.  Elements of X_0 below 2^-46 count as zero (a
+ * matrix whose norm is that far below eps).  Infinities and NaN in a matrix make that matrix's
+ * result NaN or zero, as in the formula, and touch no other matrix.
+ * ------------------------------------------------------------------- */
+
+#define ZR_DTYPE_F32 0
+#define ZR_DTYPE_BF16 1
+#define ZR_DTYPE_F16 2
+
+/* Coefficients and count of the iteration.  steps 1..32; eps in
+ * [1e-30, 1]; the coefficients must keep every iterate of singular values in
+ * [0, 1] inside fp16's range (|X| <= 31, |b s + c s^2| <= 31 for every
+ * singular value squared s, s <= 15); Muon's are (3.4445, -4.7750, 2.0315). */
+typedef struct {
+    float a, b, c, eps;
+    int32_t steps;
+} zr_newton_schulz;
+
+/* Orthogonalises a batch of m x n matrices: element (i, r, c) of x is at
+ * x[i * x_batch_stride + r * x_row_stride + c] (elements; the columns are
+ * contiguous; strides may be any non-negative numbers, so rows and matrices
+ * may repeat), of dtype ZR_DTYPE_*; out likewise, always bf16, whose rows
+ * must not overlap (out_row_stride >= n, out_batch_stride >= (m - 1) *
+ * out_row_stride + n; strides of an extent of 1 are not looked at).  out may
+ * be x itself with the same strides; otherwise they must not overlap.  x and
+ * out need their element's alignment only.  batch, m or n of 0: nothing to
+ * do, ZR_OK.
+ * The workspace (zr_orthogonalize_workspace_bytes, 256-byte aligned) holds
+ * fp16 copies; calls that share one must be ordered on the GPU.  Its first
+ * 32-bit word is 0 after a completed call; 1 says that a wait inside a
+ * kernel ran out and the results are not valid (not expected; the
+ * alternative would be a hang).
+ * Errors: ZR_ERR_INVALID_ARG (NULL, negative sizes or strides, dtype,
+ * coefficients, overlapping output rows), ZR_ERR_ALIGNMENT,
+ * ZR_ERR_NO_WORKSPACE (too small), ZR_ERR_UNSUPPORTED (an extent or the batch
+ * above 2^24, the smaller extent above 2^17, more than 2e12 elements; not
+ * compute capability 10.x), ZR_ERR_CUDA. */
+zr_status zr_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, uint64_t* bytes);
+zr_status zr_orthogonalize(const void* x, int32_t dtype, int64_t batch, int64_t m, int64_t n,
+                           int64_t x_batch_stride, int64_t x_row_stride, void* out, int64_t out_batch_stride,
+                           int64_t out_row_stride, const zr_newton_schulz* ns, void* d_workspace,
+                           uint64_t workspace_bytes, zr_stream_t stream);
+
+/* The Muon step for one rank's matrices, in place of stages 2 and 3 of
+ * zr_step: per owned element (fp32, one rounding per operation)
+ *   g = (g_0 + ... + g_{W-1}) / W      as in zr_step
+ *   M = momentum * M + g
+ *   U = g + momentum * M  (nesterov),  or M
+ * then per matrix O = the orthogonalisation of U, and
+ *   p = p * (1 - lr * weight_decay) - (lr * s) * O
+ *   param_out = bf16(p)
+ * with s = sqrt(max(1, m / n)) (ZR_MUON_SCALE_SPECTRAL) or
+ * 0.2 sqrt(max(m, n)) (ZR_MUON_SCALE_RMS: an update of AdamW's usual size).
+ * A tensor's last two extents are the matrix, leading ones a batch of
+ * matrices. */
+#define ZR_MUON_SCALE_SPECTRAL 0
+#define ZR_MUON_SCALE_RMS 1
+typedef struct {
+    float lr, momentum, weight_decay;
+    int32_t nesterov, scale;
+    zr_newton_schulz ns;
+} zr_muon_params;
+
+/* How the momentum is held.  ZR_MOMENTUM_F32: owned_numel floats in owned
+ * order.  ZR_MOMENTUM_INT8: owned_numel int8 codes in owned order and one
+ * fp32 scale for every 256 consecutive elements of a matrix (its last block
+ * may be shorter; matrices in owned order, zr_muon_scales entries in all):
+ * scale = max|M| / 127 over the block, code = M / scale rounded to nearest
+ * even, value = code * scale.  A block with an infinity or NaN reads back as
+ * NaN throughout. */
+#define ZR_MOMENTUM_F32 0
+#define ZR_MOMENTUM_INT8 1
+
+typedef struct zr_muon zr_muon;
+
+/* A Muon step on `plan`'s partition, replicas, gather targets and parameter
+ * layout (the current ones at each call); the plan must outlive it and have
+ * its workspace bound before zr_muon_set_workspace.  The plan owns whole
+ * tensors (ZR_PARTITION_WHOLE_TENSOR, or W = 1), does not clip, and every
+ * tensor with elements, on any rank, has at least two extents; put other
+ * tensors in a plan of their own and step them with zr_step.  *params is
+ * copied.  Checked mode does not cover this step: it reads tables of its
+ * own.  Errors: ZR_ERR_INVALID_ARG (NULL, a vector or scalar among the
+ * tensors, momentum outside [0, 1), a negative or non-finite lr or
+ * weight_decay, coefficients, format), ZR_ERR_UNSUPPORTED (flat partition of
+ * several ranks, clipping, a shape zr_orthogonalize would refuse). */
+zr_status zr_muon_create(const zr_plan* plan, const zr_muon_params* params, int32_t momentum_format, zr_muon** out);
+void zr_muon_destroy(zr_muon* muon);
+/* New parameters for the calls that follow (a learning-rate schedule).  They
+ * travel by value: a captured graph keeps those current at capture. */
+zr_status zr_muon_set_params(zr_muon* muon, const zr_muon_params* params);
+/* Scales of a ZR_MOMENTUM_INT8 state (either format may ask). */
+zr_status zr_muon_scales(const zr_muon* muon, int64_t* n_scales);
+/* Device workspace: tables, norms, and per matrix two fp16 copies with their
+ * rounding errors and two Gram matrices (about 8 bytes per owned element and
+ * 4 per element of the Gram matrices).  zr_muon_set_workspace uploads the
+ * tables on `stream` and binds it, 256-byte aligned; steps that share one
+ * must be ordered on the GPU.  Errors as zr_plan_set_workspace. */
+zr_status zr_muon_workspace_bytes(const zr_muon* muon, uint64_t* bytes);
+zr_status zr_muon_set_workspace(zr_muon* muon, void* d_workspace, uint64_t bytes, zr_stream_t stream);
+/* One step.  grad_ptrs, master, param_out as zr_step's; momentum: the fp32
+ * state or the int8 codes; momentum_scales: the scales (ZR_MOMENTUM_INT8
+ * only, else NULL).  Updated in place, all 16-byte aligned.  Asynchronous on
+ * `stream`; may be captured in a graph.  Errors as zr_step. */
+zr_status zr_muon_step(const zr_muon* muon, const void* const* grad_ptrs, float* master, void* momentum,
+                       float* momentum_scales, void* param_out, zr_stream_t stream);
+/* An fp32 momentum (owned order) to int8 codes and scales, and back: to
+ * resume from, or save, an fp32 state.  Either format's handle.  A state that
+ * has been read back and is quantised again keeps its codes and scales
+ * wherever no value is subnormal.  Errors as zr_muon_step. */
+zr_status zr_muon_quantize_momentum(const zr_muon* muon, const float* momentum, void* codes, float* scales,
+                                    zr_stream_t stream);
+zr_status zr_muon_dequantize_momentum(const zr_muon* muon, const void* codes, const float* scales, float* momentum,
+                                      zr_stream_t stream);
+/* *gave_up = 1 if a wait inside a step's kernels ever ran out since the
+ * workspace was bound (the state is then not valid; not expected).
+ * Synchronises `stream`. */
+zr_status zr_muon_check_result(const zr_muon* muon, int32_t* gave_up, zr_stream_t stream);
+
 void zr_plan_destroy(zr_plan* plan);
 
 const char* zr_status_string(zr_status status);

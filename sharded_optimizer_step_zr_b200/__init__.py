@@ -46,10 +46,20 @@ EXPORTED = [
     "zr_debug_reduce", "zr_debug_average_check", "zr_step_no_alloc", "zr_state_save", "zr_state_load", "zr_state_reshard",
     "zr_state_export_params", "zr_plan_set_checked", "zr_plan_verify", "zr_plan_check_result",
     "zr_plan_set_param_layout", "zr_gather_params", "zr_plan_owner_offsets",
-    "zr_plan_set_gather_targets", "zr_ipc_export", "zr_ipc_open", "zr_ipc_close", "zr_plan_destroy",
+    "zr_plan_set_gather_targets", "zr_ipc_export", "zr_ipc_open", "zr_ipc_close",
+    "zr_orthogonalize_workspace_bytes", "zr_orthogonalize", "zr_muon_create", "zr_muon_destroy",
+    "zr_muon_set_params", "zr_muon_scales", "zr_muon_workspace_bytes", "zr_muon_set_workspace", "zr_muon_step",
+    "zr_muon_quantize_momentum", "zr_muon_dequantize_momentum", "zr_muon_check_result", "zr_plan_destroy",
     "zr_status_string",
 ]
 ZR_NO_ALLOC_SCRATCH_BYTES = 4 << 20
+ZR_DTYPE_F32 = 0
+ZR_DTYPE_BF16 = 1
+ZR_DTYPE_F16 = 2
+ZR_MUON_SCALE_SPECTRAL = 0
+ZR_MUON_SCALE_RMS = 1
+ZR_MOMENTUM_F32 = 0
+ZR_MOMENTUM_INT8 = 1
 
 
 class zr_check_result(ctypes.Structure):
@@ -72,6 +82,15 @@ class zr_segment(ctypes.Structure):
 class zr_ipc_handle(ctypes.Structure):
     _fields_ = [("handle", ctypes.c_ubyte * 64), ("offset", ctypes.c_uint64),
                 ("allocation_bytes", ctypes.c_uint64)]
+
+
+class zr_newton_schulz(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("a", "b", "c", "eps")] + [("steps", ctypes.c_int32)]
+
+
+class zr_muon_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("lr", "momentum", "weight_decay")] + \
+        [("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32), ("ns", zr_newton_schulz)]
 
 
 _vp, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
@@ -109,12 +128,26 @@ _lib.zr_plan_set_gather_targets.argtypes = [_vp, _vp, _vp]
 _lib.zr_ipc_export.argtypes = [_vp, _P(zr_ipc_handle)]
 _lib.zr_ipc_open.argtypes = [_P(zr_ipc_handle), _P(_vp)]
 _lib.zr_ipc_close.argtypes = [_vp]
+_lib.zr_orthogonalize_workspace_bytes.argtypes = [_i64, _i64, _i64, _P(_u64)]
+_lib.zr_orthogonalize.argtypes = [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _P(zr_newton_schulz),
+                                  _vp, _u64, _vp]
+_lib.zr_muon_create.argtypes = [_vp, _P(zr_muon_params), _i32, _P(_vp)]
+_lib.zr_muon_destroy.argtypes = [_vp]
+_lib.zr_muon_destroy.restype = None
+_lib.zr_muon_set_params.argtypes = [_vp, _P(zr_muon_params)]
+_lib.zr_muon_scales.argtypes = [_vp, _P(_i64)]
+_lib.zr_muon_workspace_bytes.argtypes = [_vp, _P(_u64)]
+_lib.zr_muon_set_workspace.argtypes = [_vp, _vp, _u64, _vp]
+_lib.zr_muon_step.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.zr_muon_quantize_momentum.argtypes = [_vp, _vp, _vp, _vp, _vp]
+_lib.zr_muon_dequantize_momentum.argtypes = [_vp, _vp, _vp, _vp, _vp]
+_lib.zr_muon_check_result.argtypes = [_vp, _P(_i32), _vp]
 _lib.zr_plan_destroy.argtypes = [_vp]
 _lib.zr_plan_destroy.restype = None
 _lib.zr_status_string.argtypes = [ctypes.c_int]
 _lib.zr_status_string.restype = ctypes.c_char_p
 for _name in EXPORTED:
-    if _name not in ("zr_plan_destroy", "zr_status_string"):
+    if _name not in ("zr_plan_destroy", "zr_muon_destroy", "zr_status_string"):
         getattr(_lib, _name).restype = ctypes.c_int
 
 
@@ -403,3 +436,86 @@ def raw_call(name: str, *args) -> int:
 
 def lib_handle():
     return _lib
+
+
+def _newton_schulz(coeffs, eps, steps) -> zr_newton_schulz:
+    a, b, c = (float(x) for x in coeffs)
+    return zr_newton_schulz(a, b, c, float(eps), int(steps))
+
+
+def zr_orthogonalize_workspace_bytes(batch: int, m: int, n: int) -> int:
+    out = _u64()
+    _check(_lib.zr_orthogonalize_workspace_bytes(int(batch), int(m), int(n), ctypes.byref(out)),
+           "zr_orthogonalize_workspace_bytes")
+    return out.value
+
+
+def zr_orthogonalize(x, dtype: int, batch: int, m: int, n: int, x_batch_stride: int, x_row_stride: int, out,
+                     out_batch_stride: int, out_row_stride: int, coeffs, eps: float, steps: int, workspace,
+                     workspace_bytes: int, stream=None) -> None:
+    ns = _newton_schulz(coeffs, eps, steps)
+    _check(_lib.zr_orthogonalize(_addr(x), dtype, batch, m, n, x_batch_stride, x_row_stride, _addr(out),
+                                 out_batch_stride, out_row_stride, ctypes.byref(ns), _addr(workspace),
+                                 workspace_bytes, _stream(stream)), "zr_orthogonalize")
+
+
+def _muon_params(lr, momentum, weight_decay, nesterov, scale, coeffs, eps, steps) -> zr_muon_params:
+    return zr_muon_params(lr, momentum, weight_decay, 1 if nesterov else 0, int(scale),
+                          _newton_schulz(coeffs, eps, steps))
+
+
+def zr_muon_create(plan: int, lr: float, momentum: float, weight_decay: float, nesterov: bool, scale: int, coeffs,
+                   eps: float, steps: int, momentum_format: int) -> int:
+    """Returns the handle (an integer); release it with zr_muon_destroy."""
+    hp = _muon_params(lr, momentum, weight_decay, nesterov, scale, coeffs, eps, steps)
+    out = ctypes.c_void_p()
+    _check(_lib.zr_muon_create(plan, ctypes.byref(hp), int(momentum_format), ctypes.byref(out)), "zr_muon_create")
+    return out.value
+
+
+def zr_muon_destroy(muon: int) -> None:
+    _lib.zr_muon_destroy(muon)
+
+
+def zr_muon_set_params(muon: int, lr: float, momentum: float, weight_decay: float, nesterov: bool, scale: int,
+                       coeffs, eps: float, steps: int) -> None:
+    hp = _muon_params(lr, momentum, weight_decay, nesterov, scale, coeffs, eps, steps)
+    _check(_lib.zr_muon_set_params(muon, ctypes.byref(hp)), "zr_muon_set_params")
+
+
+def zr_muon_scales(muon: int) -> int:
+    out = _i64()
+    _check(_lib.zr_muon_scales(muon, ctypes.byref(out)), "zr_muon_scales")
+    return out.value
+
+
+def zr_muon_workspace_bytes(muon: int) -> int:
+    out = _u64()
+    _check(_lib.zr_muon_workspace_bytes(muon, ctypes.byref(out)), "zr_muon_workspace_bytes")
+    return out.value
+
+
+def zr_muon_set_workspace(muon: int, workspace, nbytes: int, stream=None) -> None:
+    _check(_lib.zr_muon_set_workspace(muon, _addr(workspace), int(nbytes), _stream(stream)), "zr_muon_set_workspace")
+
+
+def zr_muon_step(muon: int, grads, master, momentum, momentum_scales, param_out, stream=None) -> None:
+    _check(_lib.zr_muon_step(muon, _ptr_array(grads), _addr(master), _addr(momentum), _addr(momentum_scales),
+                             _addr(param_out), _stream(stream)), "zr_muon_step")
+
+
+def zr_muon_quantize_momentum(muon: int, momentum, codes, scales, stream=None) -> None:
+    _check(_lib.zr_muon_quantize_momentum(muon, _addr(momentum), _addr(codes), _addr(scales), _stream(stream)),
+           "zr_muon_quantize_momentum")
+
+
+def zr_muon_dequantize_momentum(muon: int, codes, scales, momentum, stream=None) -> None:
+    _check(_lib.zr_muon_dequantize_momentum(muon, _addr(codes), _addr(scales), _addr(momentum), _stream(stream)),
+           "zr_muon_dequantize_momentum")
+
+
+def zr_muon_check_result(muon: int, stream=None) -> bool:
+    """True if a wait inside a step's kernels ever ran out."""
+    out = _i32()
+    _check(_lib.zr_muon_check_result(muon, ctypes.byref(out), _stream(stream)), "zr_muon_check_result")
+    return out.value != 0

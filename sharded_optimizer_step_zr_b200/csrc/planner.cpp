@@ -245,6 +245,8 @@ zr_status build_plan(zr_plan& p, int32_t n_tensors, const int32_t* ndims,
     p.n_tensors = n_tensors;
     p.numel.assign(n_tensors, 0);
     p.goff.assign(n_tensors, 0);
+    p.rows.assign(n_tensors, -1);
+    p.cols.assign(n_tensors, -1);
     int64_t total = 0;
     for (int32_t t = 0; t < n_tensors; ++t) {
         if (ndims[t] < 0 || (ndims[t] > 0 && shapes[t] == nullptr)) return ZR_ERR_INVALID_ARG;
@@ -254,6 +256,10 @@ zr_status build_plan(zr_plan& p, int32_t n_tensors, const int32_t* ndims,
             if (mul_overflows(n, shapes[t][d], &n)) return ZR_ERR_INVALID_ARG;
         }
         p.numel[t] = n;
+        if (ndims[t] >= 2) {
+            p.rows[t] = shapes[t][ndims[t] - 2];
+            p.cols[t] = shapes[t][ndims[t] - 1];
+        }
         p.goff[t] = total;
         if (n > std::numeric_limits<int64_t>::max() - total) return ZR_ERR_INVALID_ARG;
         total += n;

@@ -146,7 +146,8 @@ int launch_clip_combine(const ClipArgs& c, void* stream);
 
 // W's scalars in the launch arguments: the count, whether it is a power of
 // two, and 1/W rounded to nearest (IEEE single division on the host).
-inline void set_world_size(LaunchArgs& a, int32_t W) {
+template <typename Args>
+inline void set_world_size(Args& a, int32_t W) {
     a.world_size = W;
     a.w_is_pow2 = (W & (W - 1)) == 0 ? 1 : 0;
     a.inv_w = 1.0f / static_cast<float>(W);
@@ -197,6 +198,7 @@ struct zr_plan {
     zr_adamw hp{};
 
     std::vector<int64_t> numel;          // per tensor
+    std::vector<int64_t> rows, cols;     // per tensor: the last two extents (rows -1: fewer than two)
     std::vector<int64_t> goff;           // per tensor, global layout
     std::vector<int32_t> tensor_owner;   // whole-tensor mode
     std::vector<int32_t> tensor_bucket;
