@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -48,47 +49,55 @@ constexpr float kNsScaleB = 1024.0f;
 constexpr float kNsScaleLo = 2048.0f;   // stored error = (X * kNsScaleX - stored X) * kNsScaleLo
 
 // ---------------------------------------------------------------------------
-// product kernel: shapes
+// the iteration kernel: shapes
 // ---------------------------------------------------------------------------
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
-constexpr int kBoxBytes = 64 * 64 * 2;                     // one TMA box: 64 rows of 128 bytes
-constexpr int kOp1Bytes = kBM / 64 * kBoxBytes;            // 16 KB
-constexpr int kOp2Bytes = kBN / 64 * kBoxBytes;            // 32 KB
-constexpr int kStageBytes = kOp1Bytes + kOp2Bytes;
-constexpr int kGemmThreads = 192;                          // producer, issuer, four epilogue warps
-constexpr int kGemmSmem = kStages * kStageBytes + 1024;    // + alignment to a swizzle atom
+constexpr int kBM = 256;                                   // rows of a tile: 128 on each CTA of a pair
+constexpr int kBN = 256;                                   // columns, or half as many for launches of few tiles
+constexpr int kBK = 64;
+constexpr int kStages = 5;
+constexpr int kBoxBytes = 64 * 64 * 2;                     // one operand box: 64 rows of 128 bytes
+constexpr int kOpBytes = 2 * kBoxBytes;                    // a CTA's 128 rows of op1, or its half (128 or 64) of op2's
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kEpiWarps = 4;
+constexpr int kPartBytes = 32 * 128;                       // a warp's 32 rows of 64 fp16 columns
+constexpr int kBufBytes = 2 * kPartBytes;                  // X and its rounding error; or a result and its mirror image; or 32 x 64 fp32
+constexpr int kWarpBytes = 2 * kBufBytes;
+constexpr int kIterThreads = 64 + 32 * kEpiWarps;          // producer, issuer, epilogue warps
+constexpr int kIterSmem = kStages * kStageBytes + kEpiWarps * kWarpBytes + 1024;   // + alignment to a swizzle atom
 constexpr int kMaxGroups = 16;
 
-enum class Ns : int { kGram = 0, kPoly = 1, kUpdate = 2, kOut = 3, kApply = 4 };
+enum : int { kGram = 0, kPoly = 1, kUpdate = 2 };          // products of a step, in order
 
-// One group's share of a launch: D = op1 op2^T, D rows x cols, K = k.
-struct GemmGroup {
-    CUtensorMap op1, op2;
-    int32_t rows, cols, k;
-    int32_t op1_mn, op2_mn;           // operand stored with its contraction extent as rows
-    int32_t tiles_n, tiles_per_matrix, first_tile;
-    int64_t ld, slot;                 // row pitch and matrix pitch of in and out
-    const uint16_t *in_hi, *in_lo;    // A (kPoly) or X (kUpdate, kOut, kApply)
-    uint16_t *out_hi, *out_lo;
-    const float* diag_in;             // A's (kPoly) or B's (kUpdate, kOut, kApply)
-    float* diag_out;                  // A's (kGram) or B's (kPoly)
-    int32_t diag_rows;                // B acts on X's rows (wide), not its columns
-    int64_t out_row, out_batch;       // kOut
-    const int64_t *master_offsets, *param_offsets;   // kApply
+struct IterGroup {
+    NsMaps maps;
+    int32_t m, n, dim, tall;
+    int32_t sym_tiles, out_tiles, out_tiles_n;             // tiles of a matrix: A and A A; the update
+    int64_t first_sym, first_out;                          // the group's first tile of a product
+    uint32_t* done;                                        // per matrix: finished warps' shares of tiles
+    float *gram_diag, *poly_diag;
+    uint16_t* out;                                         // the last update's result in bf16
+    int64_t out_row, out_batch;
+    int32_t out_vec;                                       // its rows and matrices start 16-byte aligned
+    const int64_t *master_offsets, *param_offsets;
     float step_size;
 };
 
-struct GemmLaunch {
-    int32_t n_groups, total_tiles;
-    float alpha, beta, gamma, decay;   // of the accumulator, the elementwise term, the diagonals; kApply
-    uint32_t* gave_up;
+struct Affine { float alpha, beta, gamma; };               // of the accumulator, the elementwise term, the diagonals
+
+template <int NG>
+struct IterLaunch {
+    int32_t n_groups, steps, pairs;
+    int32_t sym_bn, out_bn;
+    int64_t sym_total, out_total;                          // tiles of all matrices
+    Affine k[4];                                           // A, B, update, last update
+    float decay;
+    uint32_t *abort_word, *gave_up;
     float* master;
     uint16_t* param_out;
     uint16_t* const* targets;
     int32_t n_targets;
-    GemmGroup g[kMaxGroups];
+    IterGroup g[NG];
 };
 
 // ---------------------------------------------------------------------------
@@ -104,8 +113,13 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ uint32_t leader_address(uint32_t addr) {     // the same address in the pair's first CTA
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -118,31 +132,87 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-
-// Waits are bounded: after kWaitTries failed tries (each blocks for up to a
-// hardware time slice) the block gives up -- the error word is set, every
-// role leaves its loop, and the kernel returns with its results unfinished.
-constexpr int kWaitTries = 1 << 20;
-constexpr int kDrainTries = 1 << 14;
-
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                          uint32_t* gave_up) {
-    if (mbar_try(bar, parity)) return true;
-    for (int i = 0; i < kWaitTries; ++i) {
-        if (mbar_try(bar, parity)) return true;
-        if ((i & 63) == 63 && *abort_flag) return false;
-    }
-    *abort_flag = 1u;
-    atomicExch(gave_up, 1u);
-    return false;
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void red_release(uint32_t* p, uint32_t v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+// Waits are bounded: a wait that lasts kWaitNs gives up -- it sets the
+// launch's abort word and the caller's status word, every role of every CTA
+// leaves its loop, and the kernel returns with its results unfinished.  The
+// longest wait of a sound launch is one product of the whole batch (a second
+// for 100000 x 100000).
+constexpr uint64_t kWaitNs = 20ull * 1000 * 1000 * 1000;
+constexpr uint32_t kWaitTries = 1u << 30;
+constexpr uint32_t kDrainTries = 1u << 14;
+
+struct Bail {
+    volatile uint32_t* local;     // shared: this CTA's flag
+    uint32_t* word;               // global: the launch's
+    uint32_t* gave_up;            // global: the caller's
+};
+
+template <typename Ready>
+__device__ __noinline__ bool wait_slow(Ready ready, const Bail& b) {
+    const uint64_t start = now_ns();
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
+        if (ready()) return true;
+        if ((i & 63) != 63) continue;
+        if (*b.local) return false;
+        if (*reinterpret_cast<volatile uint32_t*>(b.word)) break;
+        if (now_ns() - start > kWaitNs) {
+            atomicExch(b.gave_up, 1u);
+            break;
+        }
+    }
+    *b.local = 1u;
+    atomicExch(b.word, 1u);
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Bail& b) {
+    if (mbar_try(bar, parity)) return true;
+    return wait_slow([=] { return mbar_try(bar, parity); }, b);
+}
+__device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t need, const Bail& b) {
+    if (ld_acquire(p) >= need) return true;
+    return wait_slow([=] { return ld_acquire(p) >= need; }, b);
+}
+
+// An operand box; its bytes count on the leader's barrier.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 128
 // bytes (64 contraction elements), groups of 8 rows 1024 bytes apart.
@@ -159,12 +229,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Arrives on the barrier at this address in both CTAs of the pair.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
@@ -183,8 +257,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(addr) : "memory");
+    return q;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 q) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
+}
+__device__ __forceinline__ void st_shared2(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_shared2(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------------------
-// epilogue pieces
+// number formats
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint16_t half_bits(float x) {
@@ -204,175 +300,237 @@ __device__ __forceinline__ uint16_t bf16_bits(float x) {
     memcpy(&u, &h, 2);
     return u;
 }
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
+__device__ __forceinline__ float2 half2_values(uint32_t u) {
+    __half2 h;
+    memcpy(&h, &u, 4);
+    return __half22float2(h);
+}
 
-// 32 consecutive fp16 values at a 16-byte aligned address.
-__device__ __forceinline__ void ld_half32(const uint16_t* p, float (&v)[32]) {
+// Half a staged row: 32 fp16 values of row `r` from 16-byte piece `first` on,
+// in the order that the 128-byte swizzle gives the pieces.
+__device__ __forceinline__ uint32_t staged(uint32_t part, int r, int piece) {
+    return part + r * 128 + ((piece ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void ld_staged32(uint32_t part, int r, int first, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p + 8 * i);
+        const uint4 q = ld_shared16(staged(part, r, first + i));
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[8 * i + 2 * j] = half_value(static_cast<uint16_t>(w[j]));
-            v[8 * i + 2 * j + 1] = half_value(static_cast<uint16_t>(w[j] >> 16));
+            const float2 f = half2_values(w[j]);
+            v[8 * i + 2 * j] = f.x;
+            v[8 * i + 2 * j + 1] = f.y;
         }
     }
 }
-__device__ __forceinline__ void st_half32(uint16_t* p, const uint16_t (&h)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint4 q;
-        q.x = h[8 * i] | (static_cast<uint32_t>(h[8 * i + 1]) << 16);
-        q.y = h[8 * i + 2] | (static_cast<uint32_t>(h[8 * i + 3]) << 16);
-        q.z = h[8 * i + 4] | (static_cast<uint32_t>(h[8 * i + 5]) << 16);
-        q.w = h[8 * i + 6] | (static_cast<uint32_t>(h[8 * i + 7]) << 16);
-        *reinterpret_cast<uint4*>(p + 8 * i) = q;
-    }
-}
 
-// Which tile: its group, matrix and position.  Symmetric results (A, B) list
-// only tiles that touch the lower triangle: of row blocks 2p and 2p + 1 (128
-// rows each), the first p + 1 column blocks (256 columns each).
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+
+// One role's walk over the launch's tiles: product by product, in each the
+// matrices in order, every `pairs`-th tile.
 struct TileAt {
-    int32_t group, slot, row0, col0;
+    int32_t step = 0, op = 0, group = 0, slot = 0, row0 = 0, col0 = 0, bn = 0;
 };
 
-template <bool SYM>
-__device__ __forceinline__ TileAt find_tile(const GemmLaunch& L, int32_t tile) {
-    int32_t gi = 0;
-    while (gi + 1 < L.n_groups && tile >= L.g[gi + 1].first_tile) ++gi;
-    const GemmGroup& g = L.g[gi];
-    const int32_t t = tile - g.first_tile;
-    TileAt at;
-    at.group = gi;
-    at.slot = t / g.tiles_per_matrix;
-    const int32_t r = t - at.slot * g.tiles_per_matrix;
-    if constexpr (SYM) {
-        int32_t p = static_cast<int32_t>((sqrtf(4.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-        while (static_cast<int64_t>(p + 1) * (p + 2) <= r) ++p;
-        while (static_cast<int64_t>(p) * (p + 1) > r) --p;
-        const int32_t rem = r - p * (p + 1);
-        const int32_t second = rem >= p + 1 ? 1 : 0;
-        at.row0 = (2 * p + second) * kBM;
-        at.col0 = (rem - second * (p + 1)) * kBN;
-    } else {
-        at.row0 = (r / g.tiles_n) * kBM;
-        at.col0 = (r % g.tiles_n) * kBN;
+template <int NG>
+struct TileWalk {
+    const IterLaunch<NG>& L;
+    int64_t r;
+    int32_t step = 0;
+    __device__ __forceinline__ TileWalk(const IterLaunch<NG>& l, int32_t pair) : L(l), r(pair) { wrap(); }
+    __device__ __forceinline__ void wrap() {
+        const int64_t per_step = 2 * L.sym_total + L.out_total;
+        while (r >= per_step) {
+            r -= per_step;
+            ++step;
+        }
     }
-    return at;
+    __device__ __forceinline__ bool live() const { return step < L.steps; }
+    __device__ __forceinline__ void next() {
+        r += L.pairs;
+        wrap();
+    }
+    __device__ __forceinline__ TileAt at() const {
+        TileAt a;
+        a.step = step;
+        a.op = r < L.sym_total ? kGram : r < 2 * L.sym_total ? kPoly : kUpdate;
+        const int64_t t0 = r - a.op * L.sym_total;
+        int32_t gi = 0;
+        if (a.op == kUpdate) {
+            while (gi + 1 < L.n_groups && t0 >= L.g[gi + 1].first_out) ++gi;
+            const IterGroup& g = L.g[gi];
+            const int64_t t = t0 - g.first_out;
+            a.slot = static_cast<int32_t>(t / g.out_tiles);
+            const int32_t q = static_cast<int32_t>(t - static_cast<int64_t>(a.slot) * g.out_tiles);
+            a.bn = L.out_bn;
+            a.row0 = (q / g.out_tiles_n) * kBM;
+            a.col0 = (q % g.out_tiles_n) * a.bn;
+        } else {
+            // Row block i of 256 has the column tiles up to its diagonal
+            // block: i + 1 of 256 columns, or 2 (i + 1) of 128.
+            while (gi + 1 < L.n_groups && t0 >= L.g[gi + 1].first_sym) ++gi;
+            const IterGroup& g = L.g[gi];
+            const int64_t t = t0 - g.first_sym;
+            a.slot = static_cast<int32_t>(t / g.sym_tiles);
+            const int32_t q = static_cast<int32_t>(t - static_cast<int64_t>(a.slot) * g.sym_tiles);
+            a.bn = L.sym_bn;
+            const int32_t twice = a.bn == kBN ? 2 * q : q;      // i (i + 1) <= twice
+            int32_t i = static_cast<int32_t>((sqrtf(4.0f * static_cast<float>(twice) + 1.0f) - 1.0f) * 0.5f);
+            while (static_cast<int64_t>(i + 1) * (i + 2) <= twice) ++i;
+            while (static_cast<int64_t>(i) * (i + 1) > twice) --i;
+            a.row0 = i * kBM;
+            a.col0 = (q - (a.bn == kBN ? i * (i + 1) / 2 : i * (i + 1))) * a.bn;
+        }
+        a.group = gi;
+        return a;
+    }
+};
+
+// What the matrix's counter shows once everything that a tile reads is written.
+__device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const TileAt& at) {
+    const uint32_t tiles = static_cast<uint32_t>(at.step) * (2 * g.sym_tiles + g.out_tiles) + at.op * g.sym_tiles;
+    return tiles * (2 * kEpiWarps);
 }
 
 // ---------------------------------------------------------------------------
-// the product kernel
+// the iteration kernel
 // ---------------------------------------------------------------------------
 
-// One CTA per SM walks the tiles of all groups.  Warp 0 feeds a ring of four
-// 48 KB stages by TMA, warp 1 issues the tensor-core instructions into one of
-// two accumulators, warps 2 to 5 empty the other one, so a tile's epilogue
-// runs under the next tile's products.
-template <Ns MODE>
-__global__ void __launch_bounds__(kGemmThreads, 1) zr_ns_product_kernel(const __grid_constant__ GemmLaunch L) {
-    constexpr bool kSym = MODE == Ns::kGram || MODE == Ns::kPoly;
+// All products of all steps in one launch: 15 for five steps.  A pair of CTAs
+// (two SMs, tcgen05 cta_group::2) walks the tiles; tiles of a product wait
+// for their own matrix's counter of finished tiles, never for the whole grid,
+// so a batch's matrices fill each other's gaps and a small matrix pays a
+// counter's round trip where it paid a launch.  The walk is in dependency
+// order and the launch cooperative (every pair resident), so each wait ends.
+//
+// Per CTA: warp 0 feeds a ring of five 32 KB stages by TMA (128 rows of op1,
+// half of op2's columns), the leader's warp 1 issues the pair's tensor-core
+// instructions into one of two accumulators, warps 2 to 5 empty the other
+// one, so a tile's epilogue runs under the next tile's products.  256 x 256
+// tiles on a pair move 64 bytes per SM and clock at the tensor cores' full
+// rate, where 128 x 256 on one SM moved 96, which L2 does not sustain.
+//
+// An epilogue warp owns 32 rows.  Its elementwise operand comes by TMA into
+// a staging buffer of 32 x 64 and the result leaves from there by TMA, both
+// halves of a row in place; a symmetric result below the diagonal blocks is
+// staged a second time transposed.
+template <int NG, bool APPLY>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIterThreads, 1)
+zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kEpiWarps];
     __shared__ uint32_t s_tmem;
-    __shared__ volatile uint32_t s_abort;
+    __shared__ volatile uint32_t s_abort, s_ready;      // s_ready: tiles whose operands are written
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, staged_in = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+    const Bail bail{&s_abort, L.abort_word, L.gave_up};
 
     if (threadIdx.x == 0) {
         s_abort = 0u;
+        s_ready = 0u;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 4);
+            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
         }
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(staged_in + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_async_shared();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
-    // The previous kernel wrote the operands; nothing above read memory.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {
-            // ordinary stores wrote what the copies below read
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            uint32_t it = 0;
+            fence_async();       // the kernel before this one wrote X_0 by ordinary stores
+            uint32_t it = 0, seen = 0;
             bool ok = true;
-            for (int32_t tile = blockIdx.x; ok && tile < L.total_tiles; tile += gridDim.x) {
-                const TileAt at = find_tile<kSym>(L, tile);
-                const GemmGroup& g = L.g[at.group];
-                const int32_t nk = (g.k + kBK - 1) / kBK;
+            for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next()) {
+                const TileAt at = walk.at();
+                const IterGroup& g = L.g[at.group];
+                const uint32_t need = shares_before(g, at);
+                if (need != 0) {
+                    if (!count_wait(g.done + at.slot, need, bail)) break;
+                    fence_async();
+                }
+                s_ready = ++seen;
+                const bool mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
+                const CUtensorMap* x = &g.maps.x[at.step & 1];
+                const CUtensorMap* op1 = at.op == kGram ? x : at.op == kPoly ? &g.maps.gram : g.tall ? x : &g.maps.poly;
+                const CUtensorMap* op2 = at.op == kGram ? x : at.op == kPoly ? &g.maps.gram : g.tall ? &g.maps.poly : x;
+                const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
+                const int32_t nk = (k + kBK - 1) / kBK;
+                const int32_t r0 = at.row0 + rank * 128, c0 = at.col0 + rank * (at.bn / 2);
+                const int boxes2 = at.bn / 128;
                 for (int32_t kb = 0; kb < nk; ++kb, ++it) {
                     const uint32_t s = it % kStages, phase = (it / kStages) & 1;
-                    if (!mbar_wait(empty + 8 * s, phase ^ 1, &s_abort, L.gave_up)) {
+                    if (!mbar_wait(empty + 8 * s, phase ^ 1, bail)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = full + 8 * s, dst = smem + s * kStageBytes;
-                    mbar_expect(bar, kStageBytes);
+                    const uint32_t dst = smem + s * kStageBytes;
+                    if (rank == 0) mbar_expect(full + 8 * s, 2 * (kOpBytes + boxes2 * kBoxBytes));
+                    const uint32_t bar = leader_address(full + 8 * s);
                     const int k0 = kb * kBK;
 #pragma unroll
-                    for (int b = 0; b < kBM / 64; ++b) {
-                        const int r = at.row0 + 64 * b;
-                        tma_load_3d(dst + b * kBoxBytes, &g.op1, g.op1_mn ? r : k0, g.op1_mn ? k0 : r, at.slot, bar);
-                    }
-#pragma unroll
-                    for (int b = 0; b < kBN / 64; ++b) {
-                        const int c = at.col0 + 64 * b;
-                        tma_load_3d(dst + kOp1Bytes + b * kBoxBytes, &g.op2, g.op2_mn ? c : k0, g.op2_mn ? k0 : c,
-                                    at.slot, bar);
-                    }
+                    for (int b = 0; b < 2; ++b)
+                        tma_load_pair(dst + b * kBoxBytes, op1, mn1 ? r0 + 64 * b : k0, mn1 ? k0 : r0 + 64 * b, at.slot, bar);
+                    for (int b = 0; b < boxes2; ++b)
+                        tma_load_pair(dst + kOpBytes + b * kBoxBytes, op2, mn2 ? c0 + 64 * b : k0, mn2 ? k0 : c0 + 64 * b,
+                                      at.slot, bar);
                 }
             }
-            // A block that gave up may still have copies in flight into its
-            // shared memory: see them land (each ring slot's last fill).
-            if (s_abort)
-                for (uint32_t back = 1; back <= kStages && back <= it; ++back) {
-                    const uint32_t last = it - back;
-                    for (int i = 0; i < kDrainTries && !mbar_try(full + 8 * (last % kStages), (last / kStages) & 1); ++i) {}
-                }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             uint32_t it = 0, acc = 0;
             bool ok = true;
-            for (int32_t tile = blockIdx.x; ok && tile < L.total_tiles; tile += gridDim.x, ++acc) {
-                const TileAt at = find_tile<kSym>(L, tile);
-                const GemmGroup& g = L.g[at.group];
-                const int32_t nk = (g.k + kBK - 1) / kBK;
+            for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next(), ++acc) {
+                const TileAt at = walk.at();
+                const IterGroup& g = L.g[at.group];
+                const uint32_t mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
+                const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
+                const int32_t nk = (k + kBK - 1) / kBK;
                 const uint32_t buf = acc & 1;
-                if (!mbar_wait(acc_empty + 8 * buf, ((acc >> 1) & 1) ^ 1, &s_abort, L.gave_up)) break;
+                if (!mbar_wait(acc_empty + 8 * buf, ((acc >> 1) & 1) ^ 1, bail)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + buf * kBN;
                 // fp32 accumulators, fp16 operands, their majors, N / 8, M / 16
-                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(g.op1_mn) << 15) |
-                                       (static_cast<uint32_t>(g.op2_mn) << 16) | ((kBN >> 3) << 17) | ((kBM >> 4) << 24);
-                const uint32_t step1 = (g.op1_mn ? 16 * 128 : 32) >> 4, step2 = (g.op2_mn ? 16 * 128 : 32) >> 4;
+                const uint32_t idesc = (1u << 4) | (mn1 << 15) | (mn2 << 16) | (static_cast<uint32_t>(at.bn >> 3) << 17) |
+                                       ((kBM >> 4) << 24);
+                const uint32_t step1 = (mn1 ? 16 * 128 : 32) >> 4, step2 = (mn2 ? 16 * 128 : 32) >> 4;
                 for (int32_t kb = 0; kb < nk; ++kb, ++it) {
                     const uint32_t s = it % kStages, phase = (it / kStages) & 1;
-                    if (!mbar_wait(full + 8 * s, phase, &s_abort, L.gave_up)) {
+                    if (!mbar_wait(full + 8 * s, phase, bail)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t base = smem + s * kStageBytes;
-                    const uint64_t d1 = smem_desc(base, g.op1_mn), d2 = smem_desc(base + kOp1Bytes, g.op2_mn);
+                    const uint64_t d1 = smem_desc(base, mn1), d2 = smem_desc(base + kOpBytes, mn2);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         mma_f16(d, d1 + kk * step1, d2 + kk * step2, idesc, (kb | kk) != 0);
@@ -383,140 +541,292 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zr_ns_product_kernel(const __
         }
     } else {
         const int quad = warp & 3;                 // the TMEM lanes this warp may read
+        const uint32_t stage = smem + kStages * kStageBytes + quad * kWarpBytes;
+        const uint32_t in_bar = staged_in + 16 * quad;
+        const uint32_t free_bar = leader_address(acc_empty);
+        uint32_t in_phase = 0;                     // bit b: parity of buffer b's next load
         uint32_t acc = 0;
-        for (int32_t tile = blockIdx.x; tile < L.total_tiles; tile += gridDim.x, ++acc) {
-            const TileAt at = find_tile<kSym>(L, tile);
-            const GemmGroup& g = L.g[at.group];
+        for (TileWalk<NG> walk(L, pair); walk.live(); walk.next(), ++acc) {
+            const TileAt at = walk.at();
+            const IterGroup& g = L.g[at.group];
+            const bool sym = at.op != kUpdate, last = !sym && at.step + 1 == L.steps;
+            const int32_t rows = sym ? g.dim : g.m, cols = sym ? g.dim : g.n;
+            const int32_t row_w = at.row0 + rank * 128 + quad * 32, row = row_w + lane;
+            const int32_t chunks = row_w < rows ? (min(at.bn, cols - at.col0) + 63) / 64 : 0;
             const uint32_t buf = acc & 1;
-            if (!mbar_wait(acc_full + 8 * buf, (acc >> 1) & 1, &s_abort, L.gave_up)) break;
-            __syncwarp();
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int32_t row = at.row0 + quad * 32 + lane;
-            const bool live = row < g.rows;
-            const int64_t at_row = at.slot * g.slot + static_cast<int64_t>(row) * g.ld;
-#pragma unroll 1
-            for (int ch = 0; ch < kBN / 32; ++ch) {
-                const int32_t c0 = at.col0 + ch * 32;
-                if (c0 >= g.cols) break;
-                if (kSym && c0 > at.row0 + quad * 32 + 31) break;      // above the diagonal for the whole warp
-                float v[32];
-                tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN + ch * 32, v);
-                if constexpr (MODE == Ns::kGram) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= L.alpha;
-                } else if (live) {
-                    float x[32];
-                    ld_half32(g.in_hi + at_row + c0, x);
-                    if constexpr (MODE == Ns::kPoly) {
-                        // c A A + b A, A = D + R: acc = R R, x = R
-                        const float* diag = g.diag_in + static_cast<int64_t>(at.slot) * g.rows;
-                        const float dr = diag[row];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float dc = c0 + i < g.cols ? diag[c0 + i] : 0.0f;
-                            v[i] = c0 + i == row ? fmaf(fmaf(dr, L.gamma, L.beta * kNsScaleA), dr, v[i] * L.alpha)
-                                                 : fmaf(fmaf(dr + dc, L.gamma * (1.0f / kNsScaleA), L.beta), x[i], v[i] * L.alpha);
-                        }
-                    } else {
-                        float lo[32];
-                        ld_half32(g.in_lo + at_row + c0, lo);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = fmaf(lo[i], 1.0f / kNsScaleLo, x[i]);
-                        const float* diag = g.diag_in + static_cast<int64_t>(at.slot) * (g.diag_rows ? g.rows : g.cols);
-                        if (g.diag_rows) {
-                            const float d = diag[row] * L.gamma + L.beta;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = fmaf(x[i], d, v[i] * L.alpha);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float d = c0 + i < g.cols ? diag[c0 + i] * L.gamma + L.beta : 0.0f;
-                                v[i] = fmaf(x[i], d, v[i] * L.alpha);
-                            }
-                        }
+            const CUtensorMap* in_hi = at.op == kPoly ? &g.maps.egram : &g.maps.exh[at.step & 1];
+            const CUtensorMap* in_lo = &g.maps.exl[at.step & 1];
+            auto load = [&](int ch) {              // lane 0: the elementwise operand of a chunk
+                const uint32_t b = ch & 1, dst = stage + b * kBufBytes, bar = in_bar + 8 * b;
+                const int32_t x = at.col0 + ch * 64;
+                mbar_expect(bar, sym ? kPartBytes : 2 * kPartBytes);
+                tma_load(dst, in_hi, x, row_w, at.slot, bar);
+                if (!sym) tma_load(dst + kPartBytes, in_lo, x, row_w, at.slot, bar);
+            };
+            const Affine k = L.k[last ? 3 : at.op];
+            const float* diag = (at.op == kPoly ? g.gram_diag : g.poly_diag) + static_cast<int64_t>(at.slot) * g.dim;
+            const bool by_row = at.op == kPoly || !g.tall, by_col = at.op == kPoly || g.tall;   // of the diagonal
+            float dr = 0.0f;
+            if (at.op != kGram && chunks > 0) {
+                bool ok = true;
+                if (lane == 0) {
+                    ok = s_ready > acc || wait_slow([&] { return s_ready > acc; }, bail);
+                    if (ok) {
+                        (void)ld_acquire(g.done + at.slot);
+                        store_wait_read<0>();      // the buffers are free
+                        fence_async();
+                        load(0);
+                        if (chunks > 1) load(1);
                     }
                 }
-                if constexpr (kSym) {
-                    uint16_t h[32];
+                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+                if (by_row && row < rows) dr = __ldcg(diag + row);
+            }
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (acc >> 1) & 1, bail))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN;
+            const bool mirror = sym && at.col0 + at.bn <= at.row0;      // diagonal blocks are whole as they are
+            bool ok = true;
+#pragma unroll 1
+            for (int ch = 0; ch < chunks; ++ch) {
+                const uint32_t b = ch & 1, hi = stage + b * kBufBytes, lo = hi + kPartBytes;
+                const int32_t c = at.col0 + ch * 64;
+                if (at.op != kGram) {
+                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(in_bar + 8 * b, (in_phase >> b) & 1, bail)))) break;
+                    in_phase ^= 1u << b;
+                } else if (lane == 0) {
+                    store_wait_read<1>();
+                }
+                __syncwarp();
+                // v: 32 columns of the result from column c + 32 half on
+                auto compute = [&](int half, float(&v)[32]) {
+                    const int32_t c0 = c + 32 * half;
+                    tmem_ld32(tm + ch * 64 + half * 32, v);
+                    if (at.op == kGram) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) h[i] = half_bits(v[i]);
-                    uint16_t* out = g.out_hi + at.slot * g.slot;
-                    if (live) {
-                        uint16_t* p = out + static_cast<int64_t>(row) * g.ld + c0;
-                        if (c0 + 31 < row) {
-                            st_half32(p, h);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (c0 + i < row) p[i] = h[i];
-                                if (c0 + i == row) {
-                                    p[i] = 0;
-                                    g.diag_out[static_cast<int64_t>(at.slot) * g.rows + row] =
-                                        v[i] * (MODE == Ns::kGram ? 1.0f / kNsScaleA : 1.0f / kNsScaleB);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)      // the mirror image: a warp's 32 rows are contiguous there
-                            if (c0 + i < row) out[static_cast<int64_t>(c0 + i) * g.ld + row] = h[i];
+                        for (int i = 0; i < 32; ++i) v[i] *= k.alpha;
+                        return;
                     }
-                } else if constexpr (MODE == Ns::kUpdate) {
-                    if (live) {
-                        uint16_t h[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = half_bits(v[i]);
-                        st_half32(g.out_hi + at_row + c0, h);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = half_bits((v[i] - half_value(h[i])) * kNsScaleLo);
-                        st_half32(g.out_lo + at_row + c0, h);
-                    }
-                } else if constexpr (MODE == Ns::kOut) {
-                    if (live) {
-                        uint16_t* p = g.out_hi + at.slot * g.out_batch + static_cast<int64_t>(row) * g.out_row + c0;
-                        if (c0 + 32 <= g.cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-                            uint16_t h[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) h[i] = bf16_bits(v[i]);
-                            st_half32(p, h);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c0 + i < g.cols) p[i] = bf16_bits(v[i]);
-                        }
-                    }
-                } else {
-                    if (live) {
-                        const int64_t e = static_cast<int64_t>(row) * g.cols + c0;
-                        float* pm = L.master + g.master_offsets[at.slot] + e;
-                        const int64_t po = g.param_offsets[at.slot] + e;
+                    float x[32];
+                    ld_staged32(hi, lane, 4 * half, x);
+                    float dc = 0.0f;
+                    if (by_col && c0 + lane < cols) dc = __ldcg(diag + c0 + lane);
+                    if (at.op == kPoly) {
+                        // c A A + b A, A = D + R: acc = R R, x = R
+                        const float on = fmaf(dr, k.gamma, k.beta * kNsScaleA) * dr;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            if (c0 + i >= g.cols) continue;
-                            const float p = __fsub_rn(__fmul_rn(pm[i], L.decay), __fmul_rn(v[i], g.step_size));
-                            pm[i] = p;
-                            const uint16_t u = bf16_bits(p);
-                            if (L.n_targets == 0) L.param_out[po + i] = u;
-                            else
-                                for (int t = 0; t < L.n_targets; ++t) L.targets[t][po + i] = u;
+                            const float d = dr + __shfl_sync(0xFFFFFFFFu, dc, i);
+                            v[i] = fmaf(v[i], k.alpha, c0 + i == row ? on : fmaf(d, k.gamma * (1.0f / kNsScaleA), k.beta) * x[i]);
                         }
+                        return;
+                    }
+                    float e[32];
+                    ld_staged32(lo, lane, 4 * half, e);
+                    const float d0 = fmaf(dr, k.gamma, k.beta);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float d = g.tall ? fmaf(__shfl_sync(0xFFFFFFFFu, dc, i), k.gamma, k.beta) : d0;
+                        v[i] = fmaf(fmaf(e[i], 1.0f / kNsScaleLo, x[i]), d, v[i] * k.alpha);
+                    }
+                };
+                auto release = [&] {               // the accumulator is read
+                    if (ch + 1 < chunks) return;
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
+                };
+                if (!last) {
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        float v[32];
+                        compute(half, v);
+                        const int32_t c0 = c + 32 * half;
+                        if (sym && c0 <= row && row < c0 + 32) {
+                            float d = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c0 + i == row) {
+                                    d = v[i];
+                                    v[i] = 0.0f;
+                                }
+                            if (row < rows)
+                                (at.op == kGram ? g.gram_diag : g.poly_diag)[static_cast<int64_t>(at.slot) * g.dim + row] =
+                                    d * (at.op == kGram ? 1.0f / kNsScaleA : 1.0f / kNsScaleB);
+                        }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = half2_bits(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            st_shared16(staged(hi, lane, 4 * half + i), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+                        if (!sym) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 f = half2_values(w[i]);
+                                w[i] = half2_bits((v[2 * i] - f.x) * kNsScaleLo, (v[2 * i + 1] - f.y) * kNsScaleLo);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                st_shared16(staged(lo, lane, 4 * half + i),
+                                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+                        } else if (mirror) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                st_shared2(lo + (32 * half + i) * 64 + lane * 2,
+                                           static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
+                        }
+                    }
+                    release();
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (sym) {
+                            tma_store(at.op == kGram ? &g.maps.egram : &g.maps.epoly, c, row_w, at.slot, hi);
+                            if (mirror)
+                                tma_store(at.op == kGram ? &g.maps.mgram : &g.maps.mpoly, row_w, c, at.slot, lo);
+                        } else {
+                            tma_store(&g.maps.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
+                            tma_store(&g.maps.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
+                        }
+                        store_commit();
+                        if (at.op != kGram && ch + 2 < chunks) {
+                            store_wait_read<0>();
+                            load(ch + 2);
+                        }
+                    }
+                } else if constexpr (!APPLY) {
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        float v[32];
+                        compute(half, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = bf16_bits(v[8 * i + 2 * j]) | (static_cast<uint32_t>(bf16_bits(v[8 * i + 2 * j + 1])) << 16);
+                            st_shared16(staged(hi, lane, 4 * half + i), make_uint4(w[0], w[1], w[2], w[3]));
+                        }
+                    }
+                    release();
+                    __syncwarp();
+                    uint16_t* out = g.out + at.slot * g.out_batch;
+                    if (g.out_vec) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3), piece = lane & 7;
+                            const int32_t cc = c + 8 * piece;
+                            if (row_w + r >= rows || cc >= cols) continue;
+                            uint16_t* p = out + static_cast<int64_t>(row_w + r) * g.out_row + cc;
+                            const uint4 q = ld_shared16(staged(hi, r, piece));
+                            if (cc + 8 <= cols) {
+                                *reinterpret_cast<uint4*>(p) = q;
+                            } else {
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (cc + j < cols) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+                            }
+                        }
+                    } else {
+#pragma unroll 8
+                        for (int i = 0; i < 64; ++i) {
+                            const int r = i >> 1, cl = 32 * (i & 1) + lane;
+                            if (row_w + r < rows && c + cl < cols)
+                                out[static_cast<int64_t>(row_w + r) * g.out_row + c + cl] =
+                                    ld_shared2(staged(hi, r, cl >> 3) + 2 * (cl & 7));
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0 && ch + 2 < chunks) {
+                        fence_async_shared();
+                        load(ch + 2);
+                    }
+                } else {
+                    float v[2][32];
+                    compute(0, v[0]);
+                    compute(1, v[1]);
+                    release();
+                    __syncwarp();                  // the operand has been read; the result takes its place, 256 bytes a row
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float* f = &v[i >> 3][4 * (i & 7)];
+                        st_shared16(hi + lane * 256 + ((i ^ (lane & 7)) << 4),
+                                    make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+                    }
+                    __syncwarp();
+                    const int64_t e0 = static_cast<int64_t>(row_w) * cols + c + lane;
+                    float* pm = L.master + g.master_offsets[at.slot] + e0;
+                    const int64_t po = g.param_offsets[at.slot] + e0;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 32; r0 += 16) {
+                        float p[16][2];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (row_w + r0 + r < rows && c + 32 * j + lane < cols)
+                                    p[r][j] = pm[static_cast<int64_t>(r0 + r) * cols + 32 * j];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (row_w + r0 + r < rows && c + 32 * j + lane < cols) {
+                                    const int cl = 32 * j + lane;
+                                    const float o = ld_shared_f32(hi + (r0 + r) * 256 + (((cl >> 2) ^ (r & 7)) << 4) + 4 * (cl & 3));
+                                    const float q = __fsub_rn(__fmul_rn(p[r][j], L.decay), __fmul_rn(o, g.step_size));
+                                    const int64_t e = static_cast<int64_t>(r0 + r) * cols + 32 * j;
+                                    pm[e] = q;
+                                    const uint16_t u = bf16_bits(q);
+                                    if (L.n_targets == 0) L.param_out[po + e] = u;
+                                    else
+                                        for (int t = 0; t < L.n_targets; ++t) L.targets[t][po + e] = u;
+                                }
+                    }
+                    __syncwarp();
+                    if (lane == 0 && ch + 2 < chunks) {
+                        fence_async_shared();
+                        load(ch + 2);
                     }
                 }
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+            if (!ok) break;
+            if (chunks == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
+            }
+            if (!last) {
+                __syncwarp();
+                if (lane == 0) {
+                    store_wait();
+                    fence_async();
+                    __threadfence();
+                    red_release(g.done + at.slot, 1u);
+                }
+            }
         }
+        if (lane == 0) store_wait();
     }
-    // Every role is done (or gave up).  Products issued by a block that gave
-    // up drain through a commit to the first accumulator's barrier.
+    // Every role is done (or gave up).  A pair that gave up may still have
+    // copies and products in flight: the copies land within microseconds, and
+    // a commit after the products arrives when they are done.
+    __syncwarp();
     __syncthreads();
-    if (s_abort && threadIdx.x == 32) {
-        mma_commit(acc_full);
-        for (int i = 0; i < kDrainTries; ++i) (void)mbar_try(acc_full, 0);
+    if (s_abort) {
+        if (threadIdx.x == 32 && rank == 0) {
+            const uint32_t was = mbar_try(acc_full, 0) ? 1u : 0u;
+            mma_commit(acc_full);
+            for (uint32_t i = 0; i < kDrainTries && !mbar_try(acc_full, was); ++i) {}
+        }
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    __syncthreads();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---------------------------------------------------------------------------
@@ -538,9 +848,11 @@ struct PrepGroup {
     float2* scale;
     uint16_t *xh, *xl;
     int64_t ld;
+    uint32_t* done;
 };
 struct PrepLaunch {
     int32_t n_groups;
+    uint32_t* abort_word;
     int32_t total_matrices;
     double eps;
     PrepGroup g[kMaxGroups];
@@ -657,6 +969,10 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_start_kernel(const __grid_
     asm volatile("griddepcontrol.launch_dependents;");
     const PieceAt at = find_piece(L);
     const PrepGroup& g = L.g[at.group];
+    if (threadIdx.x == 0 && at.piece == 0) {       // the iteration kernel's words
+        g.done[at.slot] = 0u;
+        if (at.group == 0 && at.slot == 0) *L.abort_word = 0u;
+    }
     if (at.col >= g.cols) return;
     const float2 s = g.scale[at.slot];
     const int64_t out = (static_cast<int64_t>(at.slot) * g.rows + at.row0) * g.ld + at.col;
@@ -701,29 +1017,33 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A batch of rows x cols fp16 matrices with rows of ld elements, read in
-// boxes of 64 x 64; what lies outside a matrix reads as zero.
-int encode_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld) {
+// A batch of rows x cols fp16 matrices with rows of ld elements, copied in
+// boxes of box_cols x box_rows; what lies outside a matrix reads as zero and
+// is not written.
+int encode_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld, int box_cols = 64,
+               int box_rows = 64, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(batch)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
-    const cuuint32_t box[3] = {64, 64, 1}, unit[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t unit[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
 
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
-int32_t symmetric_tiles(int64_t g) {
-    const int64_t r = (g + kBM - 1) / kBM, p = r / 2;
-    return static_cast<int32_t>(p * (p + 1) + (r % 2 ? p + 1 : 0));
+// Tiles of a symmetric result (row blocks of 256, the columns up to the
+// diagonal block; only the last row block may have fewer) and of a full one.
+int64_t symmetric_tiles(int64_t g, int bn) {
+    const int64_t i = (g + kBM - 1) / kBM;
+    return i * (i - 1) / 2 * (kBM / bn) + (g + bn - 1) / bn;
 }
-int64_t full_tiles(int64_t rows, int64_t cols) { return ((rows + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN); }
+int64_t full_tiles(int64_t rows, int64_t cols, int bn) { return ((rows + kBM - 1) / kBM) * ((cols + bn - 1) / bn); }
 
 template <typename Launch>
 struct Dependent {
@@ -742,74 +1062,104 @@ struct Dependent {
     cudaError_t run(void (*kernel)(Launch), const Launch& l) { return cudaLaunchKernelEx(&cfg, kernel, l); }
 };
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 148;
+// CTA pairs that run at once, with the kernel's shared memory allowed on the
+// device; 0 on failure.
+template <int NG, bool APPLY>
+int resident_pairs() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    auto kernel = zr_ns_iterate_kernel<NG, APPLY>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kIterSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kIterThreads);
+    cfg.dynamicSmemBytes = kIterSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+    known[dev].store(n, std::memory_order_release);
     return n;
 }
 
-template <Ns MODE>
-int launch_product(GemmLaunch& L, const NsGroup* groups, int32_t n, int32_t from, void* stream) {
-    int64_t tiles = 0;
+// 256-column tiles, or 128 where that gives the pairs an evener share: a
+// half tile costs a little over half a tile.
+int pick_columns(int64_t tiles256, int64_t tiles128, int64_t pairs) {
+    const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
+    return 0.55 * static_cast<double>(waves128) < static_cast<double>(waves256) ? 128 : 256;
+}
+
+template <int NG, bool APPLY>
+int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float coeffs[3], const NsApply& apply,
+                   uint32_t* gave_up, void* stream) {
+    const int most = resident_pairs<NG, APPLY>();
+    if (most == 0) return cudaErrorLaunchOutOfResources;
+    const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
+    IterLaunch<NG> L{};
     L.n_groups = n;
+    L.steps = steps;
+    L.k[kGram] = {kNsScaleA / (kNsScaleX * kNsScaleX), 0.0f, 0.0f};
+    L.k[kPoly] = {c * (kNsScaleB / (kNsScaleA * kNsScaleA)), b * (kNsScaleB / kNsScaleA), c * kNsScaleB};
+    L.k[kUpdate] = {1.0f / kNsScaleB, a, 1.0f};
+    L.k[3] = {1.0f / (kNsScaleB * kNsScaleX), a / kNsScaleX, 1.0f / kNsScaleX};
+    L.decay = apply.decay;
+    L.abort_word = groups[0].done + groups[0].batch;
+    L.gave_up = gave_up;
+    L.master = apply.master;
+    L.param_out = apply.param_out;
+    L.targets = apply.targets;
+    L.n_targets = apply.n_targets;
+    int64_t sym[2] = {0, 0}, out[2] = {0, 0};
+    for (int32_t i = 0; i < n; ++i)
+        for (int h = 0; h < 2; ++h) {
+            sym[h] += groups[i].batch * symmetric_tiles(groups[i].gram_dim(), kBN >> h);
+            out[h] += groups[i].batch * full_tiles(groups[i].m, groups[i].n, kBN >> h);
+        }
+    L.sym_bn = pick_columns(sym[0], sym[1], most);
+    L.out_bn = pick_columns(out[0], out[1], most);
     for (int32_t i = 0; i < n; ++i) {
         const NsGroup& s = groups[i];
-        GemmGroup& g = L.g[i];
-        const bool wide = s.m <= s.n;
-        const int64_t dim = s.gram_dim();
-        g.first_tile = static_cast<int32_t>(tiles);
-        if (MODE == Ns::kGram || MODE == Ns::kPoly) {
-            g.rows = g.cols = static_cast<int32_t>(dim);
-            g.op1 = g.op2 = MODE == Ns::kGram ? s.map_x[from] : s.map_gram;
-            g.k = static_cast<int32_t>(MODE == Ns::kGram ? std::max(s.m, s.n) : dim);
-            g.op1_mn = g.op2_mn = MODE == Ns::kGram && !wide;
-            g.tiles_per_matrix = symmetric_tiles(dim);
-            g.tiles_n = 0;
-            g.ld = s.ldg();
-            g.slot = dim * s.ldg();
-            g.in_hi = s.gram;
-            g.out_hi = MODE == Ns::kGram ? s.gram : s.poly;
-            g.diag_in = s.gram_diag;
-            g.diag_out = MODE == Ns::kGram ? s.gram_diag : s.poly_diag;
-        } else {
-            // wide: B X, X's rows are the contraction; tall: X B, B symmetric
-            g.rows = static_cast<int32_t>(s.m);
-            g.cols = static_cast<int32_t>(s.n);
-            g.k = static_cast<int32_t>(dim);
-            g.op1 = wide ? s.map_poly : s.map_x[from];
-            g.op2 = wide ? s.map_x[from] : s.map_poly;
-            g.op1_mn = 0;
-            g.op2_mn = wide ? 1 : 0;
-            g.tiles_n = static_cast<int32_t>((s.n + kBN - 1) / kBN);
-            g.tiles_per_matrix = static_cast<int32_t>(full_tiles(s.m, s.n));
-            g.ld = s.ld();
-            g.slot = s.m * s.ld();
-            g.in_hi = s.xh[from];
-            g.in_lo = s.xl[from];
-            g.diag_in = s.poly_diag;
-            g.diag_rows = wide ? 1 : 0;
-            if (MODE == Ns::kUpdate) {
-                g.out_hi = s.xh[from ^ 1];
-                g.out_lo = s.xl[from ^ 1];
-            } else {
-                g.out_hi = s.out;
-                g.out_row = s.out_row;
-                g.out_batch = s.out_batch;
-                g.master_offsets = s.master_offsets;
-                g.param_offsets = s.param_offsets;
-                g.step_size = s.step_size;
-            }
-        }
-        tiles += s.batch * g.tiles_per_matrix;
-        if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        IterGroup& g = L.g[i];
+        g.maps = s.maps;
+        g.m = static_cast<int32_t>(s.m);
+        g.n = static_cast<int32_t>(s.n);
+        g.dim = static_cast<int32_t>(s.gram_dim());
+        g.tall = s.m > s.n;
+        g.sym_tiles = static_cast<int32_t>(symmetric_tiles(s.gram_dim(), L.sym_bn));
+        g.out_tiles = static_cast<int32_t>(full_tiles(s.m, s.n, L.out_bn));
+        g.out_tiles_n = static_cast<int32_t>((s.n + L.out_bn - 1) / L.out_bn);
+        g.first_sym = L.sym_total;
+        g.first_out = L.out_total;
+        L.sym_total += s.batch * g.sym_tiles;
+        L.out_total += s.batch * g.out_tiles;
+        g.done = s.done;
+        g.gram_diag = s.gram_diag;
+        g.poly_diag = s.poly_diag;
+        g.out = s.out;
+        g.out_row = s.out_row;
+        g.out_batch = s.out_batch;
+        g.out_vec = reinterpret_cast<uintptr_t>(s.out) % 16 == 0 && s.out_row % 8 == 0 && s.out_batch % 8 == 0;
+        g.master_offsets = s.master_offsets;
+        g.param_offsets = s.param_offsets;
+        g.step_size = s.step_size;
     }
-    L.total_tiles = static_cast<int32_t>(tiles);
-    cudaError_t e = cudaFuncSetAttribute(zr_ns_product_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-    if (e != cudaSuccess) return e;
-    const int sms = sm_count();
-    Dependent<GemmLaunch> d(static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kGemmThreads, kGemmSmem, stream);
-    return d.run(zr_ns_product_kernel<MODE>, L);
+    L.pairs = static_cast<int32_t>(std::min<int64_t>(most, std::max(L.sym_total, L.out_total)));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(L.pairs));
+    cfg.blockDim = dim3(kIterThreads);
+    cfg.dynamicSmemBytes = kIterSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;       // every pair resident: see the kernel's waits
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, zr_ns_iterate_kernel<NG, APPLY>, L);
 }
 
 int64_t fill_prep(PrepLaunch& L, const NsGroup* groups, int32_t n) {
@@ -837,10 +1187,12 @@ int64_t fill_prep(PrepLaunch& L, const NsGroup* groups, int32_t n) {
         g.xh = s.xh[0];
         g.xl = s.xl[0];
         g.ld = s.ld();
+        g.done = s.done;
         pieces += s.batch * g.pieces_per_matrix;
         matrices += s.batch;
     }
     L.total_matrices = static_cast<int32_t>(matrices);
+    L.abort_word = groups[0].done + groups[0].batch;
     return pieces;
 }
 
@@ -858,8 +1210,9 @@ bool ns_shape_fits(int64_t batch, int64_t m, int64_t n) {
     if (total > 2.0e12) return false;
     const int64_t g = std::min(m, n);
     if (g > (1 << 17)) return false;
-    return batch * full_tiles(m, n) < (1ll << 31) && batch * ns_partials_per_matrix(m, n) < (1ll << 31) &&
-           batch * symmetric_tiles(g) < (1ll << 31);
+    // the counter of a matrix over 32 steps stays below 2^32
+    if (2 * symmetric_tiles(g, kBN / 2) + full_tiles(m, n, kBN / 2) >= (1ll << 32) / (32 * 2 * kEpiWarps)) return false;
+    return batch * ns_partials_per_matrix(m, n) < (1ll << 31);
 }
 
 uint64_t ns_scratch_bytes(int64_t batch, int64_t m, int64_t n) {
@@ -869,7 +1222,8 @@ uint64_t ns_scratch_bytes(int64_t batch, int64_t m, int64_t n) {
     g.n = n;
     const uint64_t x = align256(static_cast<uint64_t>(batch) * m * g.ld() * 2);
     const uint64_t a = align256(static_cast<uint64_t>(batch) * g.gram_dim() * g.ldg() * 2);
-    return 4 * x + 2 * a + 2 * align256(static_cast<uint64_t>(batch) * g.gram_dim() * sizeof(float));
+    return 4 * x + 2 * a + 2 * align256(static_cast<uint64_t>(batch) * g.gram_dim() * sizeof(float)) +
+           align256((static_cast<uint64_t>(batch) + 1) * sizeof(uint32_t));
 }
 
 uint64_t ns_source_offset(int64_t batch, int64_t m, int64_t n) {
@@ -889,12 +1243,28 @@ int ns_bind_scratch(NsGroup& g, void* base) {
     g.gram = reinterpret_cast<uint16_t*>(p + 4 * x);
     g.poly = reinterpret_cast<uint16_t*>(p + 4 * x + a);
     g.gram_diag = reinterpret_cast<float*>(p + 4 * x + 2 * a);
-    g.poly_diag = reinterpret_cast<float*>(
-        p + 4 * x + 2 * a + align256(static_cast<uint64_t>(g.batch) * g.gram_dim() * sizeof(float)));
+    const uint64_t d = align256(static_cast<uint64_t>(g.batch) * g.gram_dim() * sizeof(float));
+    g.poly_diag = reinterpret_cast<float*>(p + 4 * x + 2 * a + d);
+    g.done = reinterpret_cast<uint32_t*>(p + 4 * x + 2 * a + 2 * d);
+    NsMaps& t = g.maps;
     int e = cudaSuccess;
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = encode_map(&g.map_x[i], g.xh[i], g.n, g.m, g.batch, g.ld());
-    if (e == cudaSuccess) e = encode_map(&g.map_gram, g.gram, g.gram_dim(), g.gram_dim(), g.batch, g.ldg());
-    if (e == cudaSuccess) e = encode_map(&g.map_poly, g.poly, g.gram_dim(), g.gram_dim(), g.batch, g.ldg());
+    auto encode = [&](CUtensorMap* map, void* at, bool gram, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+        if (e != cudaSuccess) return;
+        e = gram ? encode_map(map, at, g.gram_dim(), g.gram_dim(), g.batch, g.ldg(), box_cols, box_rows, swizzle)
+                 : encode_map(map, at, g.n, g.m, g.batch, g.ld(), box_cols, box_rows, swizzle);
+    };
+    constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, kNone = CU_TENSOR_MAP_SWIZZLE_NONE;
+    for (int i = 0; i < 2; ++i) {
+        encode(&t.x[i], g.xh[i], false, 64, 64, k128);
+        encode(&t.exh[i], g.xh[i], false, 64, 32, k128);
+        encode(&t.exl[i], g.xl[i], false, 64, 32, k128);
+    }
+    encode(&t.gram, g.gram, true, 64, 64, k128);
+    encode(&t.poly, g.poly, true, 64, 64, k128);
+    encode(&t.egram, g.gram, true, 64, 32, k128);
+    encode(&t.epoly, g.poly, true, 64, 32, k128);
+    encode(&t.mgram, g.gram, true, 32, 64, kNone);
+    encode(&t.mpoly, g.poly, true, 32, 64, kNone);
     return e;
 }
 
@@ -924,50 +1294,22 @@ int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* 
 
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
                          const NsApply& apply, uint32_t* gave_up, void* stream) {
-    const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
     for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
         const NsGroup* gs = groups + at;
         const int32_t n = std::min(kMaxGroups, n_groups - at);
-        {
-            PrepLaunch P{};
-            const int64_t pieces = fill_prep(P, gs, n);
-            if (pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
-            Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
-            const cudaError_t e = d.run(zr_ns_start_kernel, P);
-            if (e != cudaSuccess) return e;
-        }
-        GemmLaunch L{};
-        L.gave_up = gave_up;
-        L.master = apply.master;
-        L.param_out = apply.param_out;
-        L.targets = apply.targets;
-        L.n_targets = apply.n_targets;
-        L.decay = apply.decay;
-        for (int32_t i = 0; i < steps; ++i) {
-            const int32_t from = i & 1;
-            const bool last = i + 1 == steps;
-            L.alpha = kNsScaleA / (kNsScaleX * kNsScaleX);
-            int e = launch_product<Ns::kGram>(L, gs, n, from, stream);
-            if (e != cudaSuccess) return e;
-            L.alpha = c * (kNsScaleB / (kNsScaleA * kNsScaleA));
-            L.beta = b * (kNsScaleB / kNsScaleA);
-            L.gamma = c * kNsScaleB;
-            e = launch_product<Ns::kPoly>(L, gs, n, from, stream);
-            if (e != cudaSuccess) return e;
-            if (!last) {
-                L.alpha = 1.0f / kNsScaleB;
-                L.beta = a;
-                L.gamma = 1.0f;
-                e = launch_product<Ns::kUpdate>(L, gs, n, from, stream);
-            } else {
-                L.alpha = 1.0f / (kNsScaleB * kNsScaleX);
-                L.beta = a / kNsScaleX;
-                L.gamma = 1.0f / kNsScaleX;
-                e = apply.master ? launch_product<Ns::kApply>(L, gs, n, from, stream)
-                                 : launch_product<Ns::kOut>(L, gs, n, from, stream);
-            }
-            if (e != cudaSuccess) return e;
-        }
+        PrepLaunch P{};
+        const int64_t pieces = fill_prep(P, gs, n);
+        if (pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
+        int e = d.run(zr_ns_start_kernel, P);
+        if (e != cudaSuccess) return e;
+        if (apply.master)
+            e = n == 1 ? launch_iterate<1, true>(gs, n, steps, coeffs, apply, gave_up, stream)
+                       : launch_iterate<kMaxGroups, true>(gs, n, steps, coeffs, apply, gave_up, stream);
+        else
+            e = n == 1 ? launch_iterate<1, false>(gs, n, steps, coeffs, apply, gave_up, stream)
+                       : launch_iterate<kMaxGroups, false>(gs, n, steps, coeffs, apply, gave_up, stream);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -9,6 +9,15 @@
 
 namespace zr {
 
+// Tensor maps of a group's scratch: the products' operands in boxes of 64 x
+// 64, an epilogue warp's share of X, its rounding error, A and B in boxes of
+// 64 columns x 32 rows, and the transposed shares of A and B.
+struct NsMaps {
+    CUtensorMap x[2], gram, poly;
+    CUtensorMap exh[2], exl[2], egram, epoly;
+    CUtensorMap mgram, mpoly;
+};
+
 // Matrices of one shape: source, scratch and destination.  Gram matrices
 // have the smaller extent g = min(m, n): X X^T for m <= n, X^T X otherwise.
 struct NsGroup {
@@ -36,7 +45,8 @@ struct NsGroup {
     int32_t n_partials = 0;
     const int32_t* first_partial = nullptr;   // device: batch + 1 entries, or NULL for b * n_partials
     float2* scale = nullptr;               // batch entries: X_0 = (src * x) * y, times kNsScaleX
-    CUtensorMap map_x[2], map_gram, map_poly;
+    uint32_t* done = nullptr;              // batch + 1 words: finished shares of tiles, and a launch's abort word
+    NsMaps maps;
 
     int64_t gram_dim() const { return m < n ? m : n; }
     int64_t ld() const { return (n + 63) / 64 * 64; }
