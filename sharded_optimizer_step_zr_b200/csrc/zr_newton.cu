@@ -59,18 +59,28 @@ constexpr int kStages = 5;
 constexpr int kBoxBytes = 64 * 64 * 2;                     // one operand box: 64 rows of 128 bytes
 constexpr int kOpBytes = 2 * kBoxBytes;                    // a CTA's 128 rows of op1, or its half (128 or 64) of op2's
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;                               // two for each 32 rows, taking turns at 64 columns
 constexpr int kPartBytes = 32 * 128;                       // a warp's 32 rows of 64 fp16 columns
 constexpr int kBufBytes = 2 * kPartBytes;                  // X and its rounding error; or a result and its mirror image; or 32 x 64 fp32
-constexpr int kWarpBytes = 2 * kBufBytes;
+constexpr int kDiagBytes = 64 * 4;                         // a warp's 64 columns of a diagonal
 constexpr int kIterThreads = 64 + 32 * kEpiWarps;          // producer, issuer, epilogue warps
-constexpr int kIterSmem = kStages * kStageBytes + kEpiWarps * kWarpBytes + 1024;   // + alignment to a swizzle atom
-constexpr int kMaxGroups = 16;
+constexpr int kSmemStaging = kStages * kStageBytes, kSmemDiag = kSmemStaging + kEpiWarps * kBufBytes;
+constexpr int kSmemBars = kSmemDiag + kEpiWarps * kDiagBytes;
+constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
+constexpr int kIterSmem = kSmemBars + 8 * kBars + 16;
+static_assert(kIterSmem <= 227 * 1024, "one CTA per SM");
+constexpr int kMaxGroups = 12;                             // of a launch: its parameters stay below 32 KB
 
 enum : int { kGram = 0, kPoly = 1, kUpdate = 2 };          // products of a step, in order
 
+// Tensor maps of the products' operands; pairs are for either X.
+struct IterOperands {
+    CUtensorMap gram1[2], gram2[2], poly1, poly2, update1[2], update2[2];
+};
+
 struct IterGroup {
-    NsMaps maps;
+    IterOperands op;
+    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;    // as in NsMaps
     int32_t m, n, dim, tall;
     int32_t sym_tiles, out_tiles, out_tiles_n;             // tiles of a matrix: A and A A; the update
     int64_t first_sym, first_out;                          // the group's first tile of a product
@@ -194,6 +204,12 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_chunks(uint32_t dst, const CUtensorMap* map, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -272,6 +288,12 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void ld_shared_f32x4(uint32_t addr, float (&v)[4]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint16_t ld_shared2(uint32_t addr) {
     uint16_t v;
@@ -414,24 +436,24 @@ __device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const Tile
 //
 // Per CTA: warp 0 feeds a ring of five 32 KB stages by TMA (128 rows of op1,
 // half of op2's columns), the leader's warp 1 issues the pair's tensor-core
-// instructions into one of two accumulators, warps 2 to 5 empty the other
+// instructions into one of two accumulators, warps 2 to 9 empty the other
 // one, so a tile's epilogue runs under the next tile's products.  256 x 256
 // tiles on a pair move 64 bytes per SM and clock at the tensor cores' full
 // rate, where 128 x 256 on one SM moved 96, which L2 does not sustain.
 //
-// An epilogue warp owns 32 rows.  Its elementwise operand comes by TMA into
-// a staging buffer of 32 x 64 and the result leaves from there by TMA, both
-// halves of a row in place; a symmetric result below the diagonal blocks is
+// Two epilogue warps share 32 rows.  A warp's elementwise operand comes by
+// TMA into its staging buffer of 32 x 64 and the result leaves from there by
+// TMA, both halves of a row in place; a symmetric result below the diagonal blocks is
 // staged a second time transposed.
 template <int NG, bool APPLY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIterThreads, 1)
 zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kEpiWarps];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile uint32_t s_abort, s_ready;      // s_ready: tiles whose operands are written
-    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];       // the swizzle's period
+    uint32_t* words = reinterpret_cast<uint32_t*>(smem_raw + kSmemBars + 8 * kBars);
+    uint32_t& s_tmem = words[0];
+    volatile uint32_t &s_abort = words[1], &s_ready = words[2];     // s_ready: tiles whose operands are written
+    const uint32_t smem = smem_u32(smem_raw);
+    const uint32_t full = smem + kSmemBars, empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, staged_in = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
@@ -448,7 +470,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
         }
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(staged_in + 8 * i, 1);
+        for (int i = 0; i < kEpiWarps; ++i) mbar_init(staged_in + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
     }
@@ -477,14 +499,18 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     fence_async();
                 }
                 s_ready = ++seen;
+                const int from = at.step & 1;
                 const bool mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
-                const CUtensorMap* x = &g.maps.x[at.step & 1];
-                const CUtensorMap* op1 = at.op == kGram ? x : at.op == kPoly ? &g.maps.gram : g.tall ? x : &g.maps.poly;
-                const CUtensorMap* op2 = at.op == kGram ? x : at.op == kPoly ? &g.maps.gram : g.tall ? &g.maps.poly : x;
+                const CUtensorMap* op1 = at.op == kGram ? &g.op.gram1[from] : at.op == kPoly ? &g.op.poly1 : &g.op.update1[from];
+                const CUtensorMap* op2 = at.op == kGram ? &g.op.gram2[from] : at.op == kPoly ? &g.op.poly2 : &g.op.update2[from];
                 const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
                 const int32_t nk = (k + kBK - 1) / kBK;
+                // A box of a K-major operand is 64 contraction indices x 64 or
+                // 128 rows; of an MN-major one, one or two chunks of 64 columns
+                // x 64 contraction indices (one chunk: rows as they are).
                 const int32_t r0 = at.row0 + rank * 128, c0 = at.col0 + rank * (at.bn / 2);
-                const int boxes2 = at.bn / 128;
+                const bool chunks2 = mn2 && at.bn == kBN;
+                const uint32_t bytes = 2 * (kOpBytes + at.bn / 128 * kBoxBytes);
                 for (int32_t kb = 0; kb < nk; ++kb, ++it) {
                     const uint32_t s = it % kStages, phase = (it / kStages) & 1;
                     if (!mbar_wait(empty + 8 * s, phase ^ 1, bail)) {
@@ -492,15 +518,13 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         break;
                     }
                     const uint32_t dst = smem + s * kStageBytes;
-                    if (rank == 0) mbar_expect(full + 8 * s, 2 * (kOpBytes + boxes2 * kBoxBytes));
+                    if (rank == 0) mbar_expect(full + 8 * s, bytes);
                     const uint32_t bar = leader_address(full + 8 * s);
                     const int k0 = kb * kBK;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        tma_load_pair(dst + b * kBoxBytes, op1, mn1 ? r0 + 64 * b : k0, mn1 ? k0 : r0 + 64 * b, at.slot, bar);
-                    for (int b = 0; b < boxes2; ++b)
-                        tma_load_pair(dst + kOpBytes + b * kBoxBytes, op2, mn2 ? c0 + 64 * b : k0, mn2 ? k0 : c0 + 64 * b,
-                                      at.slot, bar);
+                    if (mn1) tma_load_chunks(dst, op1, k0, r0 / 64, at.slot, bar);
+                    else tma_load_pair(dst, op1, k0, r0, at.slot, bar);
+                    if (chunks2) tma_load_chunks(dst + kOpBytes, op2, k0, c0 / 64, at.slot, bar);
+                    else tma_load_pair(dst + kOpBytes, op2, mn2 ? c0 : k0, mn2 ? k0 : c0, at.slot, bar);
                 }
             }
         }
@@ -541,10 +565,12 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
         }
     } else {
         const int quad = warp & 3;                 // the TMEM lanes this warp may read
-        const uint32_t stage = smem + kStages * kStageBytes + quad * kWarpBytes;
-        const uint32_t in_bar = staged_in + 16 * quad;
+        const int turn = (warp - 2) >> 2;          // its chunks of 64 columns: turn, turn + 2
+        const uint32_t hi = smem + kSmemStaging + (warp - 2) * kBufBytes, lo = hi + kPartBytes;
+        const uint32_t diag_cols = smem + kSmemDiag + (warp - 2) * kDiagBytes;
+        const uint32_t in_bar = staged_in + 8 * (warp - 2);
         const uint32_t free_bar = leader_address(acc_empty);
-        uint32_t in_phase = 0;                     // bit b: parity of buffer b's next load
+        uint32_t in_phase = 0;                     // parity of the next load
         uint32_t acc = 0;
         for (TileWalk<NG> walk(L, pair); walk.live(); walk.next(), ++acc) {
             const TileAt at = walk.at();
@@ -554,29 +580,27 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             const int32_t row_w = at.row0 + rank * 128 + quad * 32, row = row_w + lane;
             const int32_t chunks = row_w < rows ? (min(at.bn, cols - at.col0) + 63) / 64 : 0;
             const uint32_t buf = acc & 1;
-            const CUtensorMap* in_hi = at.op == kPoly ? &g.maps.egram : &g.maps.exh[at.step & 1];
-            const CUtensorMap* in_lo = &g.maps.exl[at.step & 1];
+            const CUtensorMap* in_hi = at.op == kPoly ? &g.egram : &g.exh[at.step & 1];
+            const CUtensorMap* in_lo = &g.exl[at.step & 1];
             auto load = [&](int ch) {              // lane 0: the elementwise operand of a chunk
-                const uint32_t b = ch & 1, dst = stage + b * kBufBytes, bar = in_bar + 8 * b;
                 const int32_t x = at.col0 + ch * 64;
-                mbar_expect(bar, sym ? kPartBytes : 2 * kPartBytes);
-                tma_load(dst, in_hi, x, row_w, at.slot, bar);
-                if (!sym) tma_load(dst + kPartBytes, in_lo, x, row_w, at.slot, bar);
+                mbar_expect(in_bar, sym ? kPartBytes : 2 * kPartBytes);
+                tma_load(hi, in_hi, x, row_w, at.slot, in_bar);
+                if (!sym) tma_load(lo, in_lo, x, row_w, at.slot, in_bar);
             };
             const Affine k = L.k[last ? 3 : at.op];
             const float* diag = (at.op == kPoly ? g.gram_diag : g.poly_diag) + static_cast<int64_t>(at.slot) * g.dim;
             const bool by_row = at.op == kPoly || !g.tall, by_col = at.op == kPoly || g.tall;   // of the diagonal
             float dr = 0.0f;
-            if (at.op != kGram && chunks > 0) {
+            if (at.op != kGram && turn < chunks) {
                 bool ok = true;
                 if (lane == 0) {
                     ok = s_ready > acc || wait_slow([&] { return s_ready > acc; }, bail);
                     if (ok) {
                         (void)ld_acquire(g.done + at.slot);
-                        store_wait_read<0>();      // the buffers are free
+                        store_wait_read<0>();      // the buffer is free
                         fence_async();
-                        load(0);
-                        if (chunks > 1) load(1);
+                        load(turn);
                     }
                 }
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
@@ -588,14 +612,20 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             const bool mirror = sym && at.col0 + at.bn <= at.row0;      // diagonal blocks are whole as they are
             bool ok = true;
 #pragma unroll 1
-            for (int ch = 0; ch < chunks; ++ch) {
-                const uint32_t b = ch & 1, hi = stage + b * kBufBytes, lo = hi + kPartBytes;
+            for (int ch = turn; ch < chunks; ch += 2) {
                 const int32_t c = at.col0 + ch * 64;
                 if (at.op != kGram) {
-                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(in_bar + 8 * b, (in_phase >> b) & 1, bail)))) break;
-                    in_phase ^= 1u << b;
+                    if (by_col) {
+                        float d[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) d[j] = c + 32 * j + lane < cols ? __ldcg(diag + c + 32 * j + lane) : 0.0f;
+                        st_shared_f32(diag_cols + 4 * lane, d[0]);
+                        st_shared_f32(diag_cols + 128 + 4 * lane, d[1]);
+                    }
+                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(in_bar, in_phase, bail)))) break;
+                    in_phase ^= 1u;
                 } else if (lane == 0) {
-                    store_wait_read<1>();
+                    store_wait_read<0>();
                 }
                 __syncwarp();
                 // v: 32 columns of the result from column c + 32 half on
@@ -609,29 +639,47 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                     float x[32];
                     ld_staged32(hi, lane, 4 * half, x);
-                    float dc = 0.0f;
-                    if (by_col && c0 + lane < cols) dc = __ldcg(diag + c0 + lane);
                     if (at.op == kPoly) {
                         // c A A + b A, A = D + R: acc = R R, x = R
-                        const float on = fmaf(dr, k.gamma, k.beta * kNsScaleA) * dr;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float d = dr + __shfl_sync(0xFFFFFFFFu, dc, i);
-                            v[i] = fmaf(v[i], k.alpha, c0 + i == row ? on : fmaf(d, k.gamma * (1.0f / kNsScaleA), k.beta) * x[i]);
+                        for (int i = 0; i < 32; i += 4) {
+                            float d[4];
+                            ld_shared_f32x4(diag_cols + 128 * half + 4 * i, d);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[i + j] *= fmaf(dr + d[j], k.gamma * (1.0f / kNsScaleA), k.beta);
                         }
+                        if (c0 == row_w) {
+                            const float on = fmaf(dr, k.gamma, k.beta * kNsScaleA) * dr;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i == lane) x[i] = on;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], k.alpha, x[i]);
                         return;
                     }
                     float e[32];
                     ld_staged32(lo, lane, 4 * half, e);
-                    const float d0 = fmaf(dr, k.gamma, k.beta);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float d = g.tall ? fmaf(__shfl_sync(0xFFFFFFFFu, dc, i), k.gamma, k.beta) : d0;
-                        v[i] = fmaf(fmaf(e[i], 1.0f / kNsScaleLo, x[i]), d, v[i] * k.alpha);
+                    for (int i = 0; i < 32; ++i) x[i] = fmaf(e[i], 1.0f / kNsScaleLo, x[i]);
+                    if (g.tall) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float d[4];
+                            ld_shared_f32x4(diag_cols + 128 * half + 4 * i, d);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[i + j] = fmaf(x[i + j], fmaf(d[j], k.gamma, k.beta), v[i + j] * k.alpha);
+                        }
+                    } else {
+                        const float d = fmaf(dr, k.gamma, k.beta);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(x[i], d, v[i] * k.alpha);
                     }
                 };
                 auto release = [&] {               // the accumulator is read
-                    if (ch + 1 < chunks) return;
+                    if (ch + 2 < chunks) return;
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
@@ -642,11 +690,11 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         float v[32];
                         compute(half, v);
                         const int32_t c0 = c + 32 * half;
-                        if (sym && c0 <= row && row < c0 + 32) {
+                        if (sym && c0 == row_w) {
                             float d = 0.0f;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (c0 + i == row) {
+                                if (i == lane) {
                                     d = v[i];
                                     v[i] = 0.0f;
                                 }
@@ -682,12 +730,12 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     __syncwarp();
                     if (lane == 0) {
                         if (sym) {
-                            tma_store(at.op == kGram ? &g.maps.egram : &g.maps.epoly, c, row_w, at.slot, hi);
+                            tma_store(at.op == kGram ? &g.egram : &g.epoly, c, row_w, at.slot, hi);
                             if (mirror)
-                                tma_store(at.op == kGram ? &g.maps.mgram : &g.maps.mpoly, row_w, c, at.slot, lo);
+                                tma_store(at.op == kGram ? &g.mgram : &g.mpoly, row_w, c, at.slot, lo);
                         } else {
-                            tma_store(&g.maps.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
-                            tma_store(&g.maps.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
+                            tma_store(&g.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
+                            tma_store(&g.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
                         }
                         store_commit();
                         if (at.op != kGram && ch + 2 < chunks) {
@@ -760,16 +808,16 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     float* pm = L.master + g.master_offsets[at.slot] + e0;
                     const int64_t po = g.param_offsets[at.slot] + e0;
 #pragma unroll 1
-                    for (int r0 = 0; r0 < 32; r0 += 16) {
-                        float p[16][2];
+                    for (int r0 = 0; r0 < 32; r0 += 8) {
+                        float p[8][2];
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
+                        for (int r = 0; r < 8; ++r)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 if (row_w + r0 + r < rows && c + 32 * j + lane < cols)
                                     p[r][j] = pm[static_cast<int64_t>(r0 + r) * cols + 32 * j];
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
+                        for (int r = 0; r < 8; ++r)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 if (row_w + r0 + r < rows && c + 32 * j + lane < cols) {
@@ -792,7 +840,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 }
             }
             if (!ok) break;
-            if (chunks == 0) {
+            if (turn >= chunks) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
             }
@@ -801,7 +849,6 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 if (lane == 0) {
                     store_wait();
                     fence_async();
-                    __threadfence();
                     red_release(g.done + at.slot, 1u);
                 }
             }
@@ -1035,6 +1082,23 @@ int encode_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t
                : cudaErrorInvalidValue;
 }
 
+// The same matrices as chunks of 64 columns, copied two at a time, 64 rows
+// each.  The last chunk reaches into the rows' padding: its columns are rows
+// or columns of a product that no result keeps.
+int encode_chunks(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>((cols + 63) / 64),
+                                static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(ld) * rows * 2};
+    const cuuint32_t box[4] = {64, 64, 2, 1}, unit[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 // Tiles of a symmetric result (row blocks of 256, the columns up to the
@@ -1125,7 +1189,22 @@ int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float 
     for (int32_t i = 0; i < n; ++i) {
         const NsGroup& s = groups[i];
         IterGroup& g = L.g[i];
-        g.maps = s.maps;
+        const NsMaps& t = s.maps;
+        const bool sym_half = L.sym_bn != kBN, out_half = L.out_bn != kBN, tall = s.m > s.n;
+        for (int j = 0; j < 2; ++j) {
+            g.op.gram1[j] = tall ? t.x_chunks[j] : t.x_rows[j];
+            g.op.gram2[j] = sym_half ? t.x_box[j] : g.op.gram1[j];
+            g.op.update1[j] = tall ? t.x_rows[j] : t.poly_rows;
+            g.op.update2[j] = tall ? (out_half ? t.poly_box : t.poly_rows) : out_half ? t.x_box[j] : t.x_chunks[j];
+            g.exh[j] = t.exh[j];
+            g.exl[j] = t.exl[j];
+        }
+        g.op.poly1 = t.gram_rows;
+        g.op.poly2 = sym_half ? t.gram_box : t.gram_rows;
+        g.egram = t.egram;
+        g.epoly = t.epoly;
+        g.mgram = t.mgram;
+        g.mpoly = t.mpoly;
         g.m = static_cast<int32_t>(s.m);
         g.n = static_cast<int32_t>(s.n);
         g.dim = static_cast<int32_t>(s.gram_dim());
@@ -1255,12 +1334,16 @@ int ns_bind_scratch(NsGroup& g, void* base) {
     };
     constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, kNone = CU_TENSOR_MAP_SWIZZLE_NONE;
     for (int i = 0; i < 2; ++i) {
-        encode(&t.x[i], g.xh[i], false, 64, 64, k128);
+        encode(&t.x_box[i], g.xh[i], false, 64, 64, k128);
+        encode(&t.x_rows[i], g.xh[i], false, 64, 128, k128);
+        if (e == cudaSuccess) e = encode_chunks(&t.x_chunks[i], g.xh[i], g.n, g.m, g.batch, g.ld());
         encode(&t.exh[i], g.xh[i], false, 64, 32, k128);
         encode(&t.exl[i], g.xl[i], false, 64, 32, k128);
     }
-    encode(&t.gram, g.gram, true, 64, 64, k128);
-    encode(&t.poly, g.poly, true, 64, 64, k128);
+    encode(&t.gram_box, g.gram, true, 64, 64, k128);
+    encode(&t.gram_rows, g.gram, true, 64, 128, k128);
+    encode(&t.poly_box, g.poly, true, 64, 64, k128);
+    encode(&t.poly_rows, g.poly, true, 64, 128, k128);
     encode(&t.egram, g.gram, true, 64, 32, k128);
     encode(&t.epoly, g.poly, true, 64, 32, k128);
     encode(&t.mgram, g.gram, true, 32, 64, kNone);

@@ -9,13 +9,13 @@
 
 namespace zr {
 
-// Tensor maps of a group's scratch: the products' operands in boxes of 64 x
-// 64, an epilogue warp's share of X, its rounding error, A and B in boxes of
-// 64 columns x 32 rows, and the transposed shares of A and B.
+// Tensor maps of a group's scratch.  The products' operands: boxes of 64
+// columns x 64 or 128 rows, and two chunks of 64 columns x 64 rows.  An
+// epilogue warp's share of X, its rounding error, A and B: 64 columns x 32
+// rows, and the transposed shares of A and B.
 struct NsMaps {
-    CUtensorMap x[2], gram, poly;
-    CUtensorMap exh[2], exl[2], egram, epoly;
-    CUtensorMap mgram, mpoly;
+    CUtensorMap x_box[2], x_rows[2], x_chunks[2], gram_box, gram_rows, poly_box, poly_rows;
+    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;
 };
 
 // Matrices of one shape: source, scratch and destination.  Gram matrices
