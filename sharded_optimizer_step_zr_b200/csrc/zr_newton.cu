@@ -128,8 +128,10 @@ __device__ __forceinline__ uint32_t leader_address(uint32_t addr) {     // the s
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
+// Orders no memory: what the arrival announces is that tensor memory has been
+// read (tcgen05.wait::ld and the fence before it).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -228,6 +230,7 @@ __device__ __forceinline__ void store_wait_read() {
 }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 128
@@ -487,7 +490,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
 
     if (warp == 0) {
         if (lane == 0) {
-            fence_async();       // the kernel before this one wrote X_0 by ordinary stores
+            fence_async_global();      // the kernel before this one wrote X_0 by ordinary stores
             uint32_t it = 0, seen = 0;
             bool ok = true;
             for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next()) {
@@ -496,7 +499,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 const uint32_t need = shares_before(g, at);
                 if (need != 0) {
                     if (!count_wait(g.done + at.slot, need, bail)) break;
-                    fence_async();
+                    fence_async_global();
                 }
                 s_ready = ++seen;
                 const int from = at.step & 1;
@@ -725,7 +728,6 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                                            static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
                         }
                     }
-                    release();
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
@@ -743,6 +745,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                             load(ch + 2);
                         }
                     }
+                    release();
                 } else if constexpr (!APPLY) {
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
@@ -848,7 +851,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 __syncwarp();
                 if (lane == 0) {
                     store_wait();
-                    fence_async();
+                    fence_async_global();
                     red_release(g.done + at.slot, 1u);
                 }
             }
