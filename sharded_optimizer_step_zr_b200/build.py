@@ -13,9 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libzr.so")
 SOURCES = ["zr_kernels.cu", "zr_scalars.cu", "zr_check.cu", "zr_gather.cu", "zr_no_alloc.cu",
-           "zr_newton.cu", "zr_muon.cu", "muon.cpp",
+           "zr_newton.cu", "zr_newton_small.cu", "zr_muon.cu", "muon.cpp",
            "planner.cpp", "api.cpp", "checkpoint.cpp", "peer.cpp"]
-HEADERS = ["zr_internal.hpp", "zr_fold.cuh", "zr_newton.hpp", "zr_muon.hpp",
+HEADERS = ["zr_internal.hpp", "zr_fold.cuh", "zr_newton.hpp", "zr_newton_ptx.cuh", "zr_muon.hpp",
            os.path.join(ROOT, "include", "zr.h"), "exports.map"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -260,11 +260,13 @@ zr_status zr_orthogonalize(const void* x, int32_t dtype, int64_t batch, int64_t 
     if (zr::ns_bind_scratch(g, base + need - zr::ns_scratch_bytes(batch, m, n)) != cudaSuccess) return ZR_ERR_CUDA;
     if (cudaMemsetAsync(base, 0, sizeof(uint32_t), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ZR_ERR_CUDA;
+    const float coeffs[3] = {ns->a, ns->b, ns->c};
+    uint32_t* gave_up = reinterpret_cast<uint32_t*>(base);
+    if (zr::ns_small(&g, 1, false))
+        return cuda_status(zr::launch_ns_small(&g, 1, ns->steps, coeffs, ns->eps, zr::NsApply(), gave_up, stream));
     int e = zr::launch_ns_sumsq(&g, 1, stream);
     if (e == cudaSuccess) e = zr::launch_ns_scales(&g, 1, ns->eps, stream);
-    const float coeffs[3] = {ns->a, ns->b, ns->c};
-    if (e == cudaSuccess)
-        e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, zr::NsApply(), reinterpret_cast<uint32_t*>(base), stream);
+    if (e == cudaSuccess) e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, zr::NsApply(), gave_up, stream);
     return cuda_status(e);
 }
 
@@ -400,11 +402,16 @@ zr_status zr_muon_step(const zr_muon* u, const void* const* grad_ptrs, float* ma
     apply.decay = static_cast<float>(1.0 - static_cast<double>(u->hp.lr) * static_cast<double>(u->hp.weight_decay));
     const int32_t n = static_cast<int32_t>(groups.size());
     int e = zr::launch_muon_momentum(a, grad_ptrs, eight, stream);
-    if (e == cudaSuccess) e = zr::launch_ns_scales(groups.data(), n, u->hp.ns.eps, stream);
+    if (e != cudaSuccess) return ZR_ERR_CUDA;
     const float coeffs[3] = {u->hp.ns.a, u->hp.ns.b, u->hp.ns.c};
+    uint32_t* gave_up = reinterpret_cast<uint32_t*>(u->d_workspace + u->at_status);
+    // Small matrices beside large ones cost the persistent kernel nothing:
+    // they run while the large ones' products wait for one another.
+    if (zr::ns_small(groups.data(), n, true))
+        return cuda_status(zr::launch_ns_small(groups.data(), n, u->hp.ns.steps, coeffs, u->hp.ns.eps, apply, gave_up, stream));
+    e = zr::launch_ns_scales(groups.data(), n, u->hp.ns.eps, stream);
     if (e == cudaSuccess)
-        e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, apply,
-                                     reinterpret_cast<uint32_t*>(u->d_workspace + u->at_status), stream);
+        e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, apply, gave_up, stream);
     return cuda_status(e);
 }
 

@@ -27,8 +27,6 @@
 // iteration (1e-2 with bf16 operands; 1.2e-3 with fp16 ones alone, and 2e-2
 // when 16 directions are 400 times stronger than the rest).
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,14 +37,10 @@
 
 #include "zr.h"
 #include "zr_newton.hpp"
+#include "zr_newton_ptx.cuh"
 
 namespace zr {
 namespace {
-
-constexpr float kNsScaleX = 1024.0f;    // stored X = X * kNsScaleX
-constexpr float kNsScaleA = 2048.0f;
-constexpr float kNsScaleB = 1024.0f;
-constexpr float kNsScaleLo = 2048.0f;   // stored error = (X * kNsScaleX - stored X) * kNsScaleLo
 
 // ---------------------------------------------------------------------------
 // the iteration kernel: shapes
@@ -93,8 +87,6 @@ struct IterGroup {
     float step_size;
 };
 
-struct Affine { float alpha, beta, gamma; };               // of the accumulator, the elementwise term, the diagonals
-
 template <int NG>
 struct IterLaunch {
     int32_t n_groups, steps, pairs;
@@ -109,252 +101,6 @@ struct IterLaunch {
     int32_t n_targets;
     IterGroup g[NG];
 };
-
-// ---------------------------------------------------------------------------
-// PTX
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ uint32_t leader_address(uint32_t addr) {     // the same address in the pair's first CTA
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-// Orders no memory: what the arrival announces is that tensor memory has been
-// read (tcgen05.wait::ld and the fence before it).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void red_release(uint32_t* p, uint32_t v) {
-    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// Waits are bounded: a wait that lasts kWaitNs gives up -- it sets the
-// launch's abort word and the caller's status word, every role of every CTA
-// leaves its loop, and the kernel returns with its results unfinished.  The
-// longest wait of a sound launch is one product of the whole batch (a second
-// for 100000 x 100000).
-constexpr uint64_t kWaitNs = 20ull * 1000 * 1000 * 1000;
-constexpr uint32_t kWaitTries = 1u << 30;
-constexpr uint32_t kDrainTries = 1u << 14;
-
-struct Bail {
-    volatile uint32_t* local;     // shared: this CTA's flag
-    uint32_t* word;               // global: the launch's
-    uint32_t* gave_up;            // global: the caller's
-};
-
-template <typename Ready>
-__device__ __noinline__ bool wait_slow(Ready ready, const Bail& b) {
-    const uint64_t start = now_ns();
-    for (uint32_t i = 0; i < kWaitTries; ++i) {
-        if (ready()) return true;
-        if ((i & 63) != 63) continue;
-        if (*b.local) return false;
-        if (*reinterpret_cast<volatile uint32_t*>(b.word)) break;
-        if (now_ns() - start > kWaitNs) {
-            atomicExch(b.gave_up, 1u);
-            break;
-        }
-    }
-    *b.local = 1u;
-    atomicExch(b.word, 1u);
-    return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Bail& b) {
-    if (mbar_try(bar, parity)) return true;
-    return wait_slow([=] { return mbar_try(bar, parity); }, b);
-}
-__device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t need, const Bail& b) {
-    if (ld_acquire(p) >= need) return true;
-    return wait_slow([=] { return ld_acquire(p) >= need; }, b);
-}
-
-// An operand box; its bytes count on the leader's barrier.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_chunks(uint32_t dst, const CUtensorMap* map, int y, int z, int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-                 ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void store_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 128
-// bytes (64 contraction elements), groups of 8 rows 1024 bytes apart.
-// MN-major: rows of 64 row-or-column elements, one per contraction index;
-// groups of 8 contraction indices 1024 bytes apart, chunks of 64 elements
-// one TMA box apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major) {
-    const uint64_t lead = mn_major ? (kBoxBytes >> 4) : 1;
-    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (lead << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrives on the barrier at this address in both CTAs of the pair.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
-    uint4 q;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(addr) : "memory");
-    return q;
-}
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 q) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
-}
-__device__ __forceinline__ void st_shared2(uint32_t addr, uint16_t v) {
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
-}
-__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void ld_shared_f32x4(uint32_t addr, float (&v)[4]) {
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint16_t ld_shared2(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// ---------------------------------------------------------------------------
-// number formats
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ uint16_t half_bits(float x) {
-    const __half h = __float2half_rn(x);
-    uint16_t u;
-    memcpy(&u, &h, 2);
-    return u;
-}
-__device__ __forceinline__ float half_value(uint16_t u) {
-    __half h;
-    memcpy(&h, &u, 2);
-    return __half2float(h);
-}
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    uint16_t u;
-    memcpy(&u, &h, 2);
-    return u;
-}
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    uint32_t u;
-    memcpy(&u, &h, 4);
-    return u;
-}
-__device__ __forceinline__ float2 half2_values(uint32_t u) {
-    __half2 h;
-    memcpy(&h, &u, 4);
-    return __half22float2(h);
-}
-
-// Half a staged row: 32 fp16 values of row `r` from 16-byte piece `first` on,
-// in the order that the 128-byte swizzle gives the pieces.
-__device__ __forceinline__ uint32_t staged(uint32_t part, int r, int piece) {
-    return part + r * 128 + ((piece ^ (r & 7)) << 4);
-}
-__device__ __forceinline__ void ld_staged32(uint32_t part, int r, int first, float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 q = ld_shared16(staged(part, r, first + i));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = half2_values(w[j]);
-            v[8 * i + 2 * j] = f.x;
-            v[8 * i + 2 * j + 1] = f.y;
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // tiles
@@ -557,7 +303,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t base = smem + s * kStageBytes;
-                    const uint64_t d1 = smem_desc(base, mn1), d2 = smem_desc(base + kOpBytes, mn2);
+                    const uint64_t d1 = smem_desc(base, mn1, kBoxBytes), d2 = smem_desc(base + kOpBytes, mn2, kBoxBytes);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         mma_f16(d, d1 + kk * step1, d2 + kk * step2, idesc, (kb | kk) != 0);
@@ -609,76 +355,90 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 if (by_row && row < rows) dr = __ldcg(diag + row);
             }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (acc >> 1) & 1, bail))) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN;
             const bool mirror = sym && at.col0 + at.bn <= at.row0;      // diagonal blocks are whole as they are
+            auto products = [&] {                  // the accumulator is complete
+                const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * buf, (acc >> 1) & 1, bail));
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                return done;
+            };
             bool ok = true;
 #pragma unroll 1
             for (int ch = turn; ch < chunks; ch += 2) {
                 const int32_t c = at.col0 + ch * 64;
-                if (at.op != kGram) {
+                // y: the elementwise term of a row's 64 columns, formed while
+                // the products still run
+                f32x2 y[2][16];
+                if (at.op == kGram) {
+                    if (lane == 0) store_wait_read<0>();
+                } else {
                     if (by_col) {
                         float d[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) d[j] = c + 32 * j + lane < cols ? __ldcg(diag + c + 32 * j + lane) : 0.0f;
                         st_shared_f32(diag_cols + 4 * lane, d[0]);
                         st_shared_f32(diag_cols + 128 + 4 * lane, d[1]);
+                        __syncwarp();
                     }
                     if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(in_bar, in_phase, bail)))) break;
                     in_phase ^= 1u;
-                } else if (lane == 0) {
-                    store_wait_read<0>();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ld_staged32(hi, lane, 4 * half, y[half]);
+                        if (at.op == kPoly) {
+                            // c A A + b A, A = D + R: acc = R R, y = b R + c (D R + R D) + (b D + c D D)
+                            const float s = k.gamma * (1.0f / kNsScaleA), base = fmaf(dr, s, k.beta);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                f32x2 d[2];
+                                ld_shared_f32x4(diag_cols + 128 * half + 8 * i, d);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    y[half][i + j] = mul2(y[half][i + j], fma2(d[j], pack2(s, s), pack2(base, base)));
+                            }
+                            if (c + 32 * half == row_w) {
+                                const float on = fmaf(dr, k.gamma, k.beta * kNsScaleA) * dr;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 f = unpack2(y[half][i]);
+                                    y[half][i] = pack2(2 * i == lane ? on : f.x, 2 * i + 1 == lane ? on : f.y);
+                                }
+                            }
+                        } else {
+                            f32x2 e[16];
+                            ld_staged32(lo, lane, 4 * half, e);
+                            constexpr float kLo = 1.0f / kNsScaleLo;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[half][i] = fma2(e[i], pack2(kLo, kLo), y[half][i]);
+                            if (g.tall) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    f32x2 d[2];
+                                    ld_shared_f32x4(diag_cols + 128 * half + 8 * i, d);
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j)
+                                        y[half][i + j] = mul2(y[half][i + j], fma2(d[j], pack2(k.gamma, k.gamma), pack2(k.beta, k.beta)));
+                                }
+                            } else {
+                                const float d = fmaf(dr, k.gamma, k.beta);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[half][i] = mul2(y[half][i], pack2(d, d));
+                            }
+                        }
+                    }
                 }
+                if (ch == turn && !(ok = products())) break;
                 __syncwarp();
                 // v: 32 columns of the result from column c + 32 half on
-                auto compute = [&](int half, float(&v)[32]) {
-                    const int32_t c0 = c + 32 * half;
+                auto result = [&](int half, f32x2(&v)[16]) {
                     tmem_ld32(tm + ch * 64 + half * 32, v);
+                    const f32x2 alpha = pack2(k.alpha, k.alpha);
                     if (at.op == kGram) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= k.alpha;
-                        return;
-                    }
-                    float x[32];
-                    ld_staged32(hi, lane, 4 * half, x);
-                    if (at.op == kPoly) {
-                        // c A A + b A, A = D + R: acc = R R, x = R
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float d[4];
-                            ld_shared_f32x4(diag_cols + 128 * half + 4 * i, d);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                x[i + j] *= fmaf(dr + d[j], k.gamma * (1.0f / kNsScaleA), k.beta);
-                        }
-                        if (c0 == row_w) {
-                            const float on = fmaf(dr, k.gamma, k.beta * kNsScaleA) * dr;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i == lane) x[i] = on;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], k.alpha, x[i]);
-                        return;
-                    }
-                    float e[32];
-                    ld_staged32(lo, lane, 4 * half, e);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = fmaf(e[i], 1.0f / kNsScaleLo, x[i]);
-                    if (g.tall) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float d[4];
-                            ld_shared_f32x4(diag_cols + 128 * half + 4 * i, d);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                v[i + j] = fmaf(x[i + j], fmaf(d[j], k.gamma, k.beta), v[i + j] * k.alpha);
-                        }
+                        for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], alpha);
                     } else {
-                        const float d = fmaf(dr, k.gamma, k.beta);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmaf(x[i], d, v[i] * k.alpha);
+                        for (int i = 0; i < 16; ++i) v[i] = fma2(v[i], alpha, y[half][i]);
                     }
                 };
                 auto release = [&] {               // the accumulator is read
@@ -688,34 +448,38 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
                 };
                 if (!last) {
-#pragma unroll 1
+#pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float v[32];
-                        compute(half, v);
-                        const int32_t c0 = c + 32 * half;
-                        if (sym && c0 == row_w) {
+                        f32x2 v[16];
+                        result(half, v);
+                        if (sym && c + 32 * half == row_w) {
                             float d = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i == lane) {
-                                    d = v[i];
-                                    v[i] = 0.0f;
-                                }
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 f = unpack2(v[i]);
+                                d = 2 * i == lane ? f.x : 2 * i + 1 == lane ? f.y : d;
+                                v[i] = pack2(2 * i == lane ? 0.0f : f.x, 2 * i + 1 == lane ? 0.0f : f.y);
+                            }
                             if (row < rows)
                                 (at.op == kGram ? g.gram_diag : g.poly_diag)[static_cast<int64_t>(at.slot) * g.dim + row] =
                                     d * (at.op == kGram ? 1.0f / kNsScaleA : 1.0f / kNsScaleB);
                         }
                         uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = half2_bits(v[2 * i], v[2 * i + 1]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 f = unpack2(v[i]);
+                            w[i] = half2_bits(f.x, f.y);
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             st_shared16(staged(hi, lane, 4 * half + i), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
                         if (!sym) {
+                            const f32x2 up = pack2(kNsScaleLo, kNsScaleLo), down = pack2(-kNsScaleLo, -kNsScaleLo);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float2 f = half2_values(w[i]);
-                                w[i] = half2_bits((v[2 * i] - f.x) * kNsScaleLo, (v[2 * i + 1] - f.y) * kNsScaleLo);
+                                const float2 h = half2_values(w[i]);
+                                const float2 f = unpack2(fma2(pack2(h.x, h.y), down, mul2(v[i], up)));
+                                w[i] = half2_bits(f.x, f.y);
                             }
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
@@ -747,16 +511,18 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                     release();
                 } else if constexpr (!APPLY) {
-#pragma unroll 1
+#pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float v[32];
-                        compute(half, v);
+                        f32x2 v[16];
+                        result(half, v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = bf16_bits(v[8 * i + 2 * j]) | (static_cast<uint32_t>(bf16_bits(v[8 * i + 2 * j + 1])) << 16);
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 f = unpack2(v[4 * i + j]);
+                                w[j] = bf16_bits(f.x) | (static_cast<uint32_t>(bf16_bits(f.y)) << 16);
+                            }
                             st_shared16(staged(hi, lane, 4 * half + i), make_uint4(w[0], w[1], w[2], w[3]));
                         }
                     }
@@ -795,17 +561,19 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         load(ch + 2);
                     }
                 } else {
-                    float v[2][32];
-                    compute(0, v[0]);
-                    compute(1, v[1]);
-                    release();
-                    __syncwarp();                  // the operand has been read; the result takes its place, 256 bytes a row
+                    // (every row's operand has been read) the result takes its place, 256 bytes a row
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float* f = &v[i >> 3][4 * (i & 7)];
-                        st_shared16(hi + lane * 256 + ((i ^ (lane & 7)) << 4),
-                                    make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+                    for (int half = 0; half < 2; ++half) {
+                        f32x2 v[16];
+                        result(half, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 f = unpack2(v[2 * i]), h = unpack2(v[2 * i + 1]);
+                            st_shared16(hi + lane * 256 + (((8 * half + i) ^ (lane & 7)) << 4),
+                                        make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(h.x), __float_as_uint(h.y)));
+                        }
                     }
+                    release();
                     __syncwarp();
                     const int64_t e0 = static_cast<int64_t>(row_w) * cols + c + lane;
                     float* pm = L.master + g.master_offsets[at.slot] + e0;
@@ -844,6 +612,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             }
             if (!ok) break;
             if (turn >= chunks) {
+                if (!products()) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
             }
@@ -990,9 +759,7 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_sumsq_kernel(const __grid_
     if (threadIdx.x == 0) g.partials[static_cast<int64_t>(at.slot) * g.n_partials + at.piece] = sum;
 }
 
-// One CTA per matrix: the norm, and 1 / (norm + eps) as two fp32 factors, a
-// power of two and the rest, so that neither leaves fp32's normal range for
-// any norm of fp32 data (a product with the power of two is exact).
+// One CTA per matrix: the norm.
 __global__ void __launch_bounds__(kPrepThreads) zr_ns_scale_kernel(const __grid_constant__ PrepLaunch L) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -1004,14 +771,7 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_scale_kernel(const __grid_
     double sum = 0.0;
     for (int64_t i = first + threadIdx.x; i < last; i += kPrepThreads) sum += __ldcg(g.partials + i);
     sum = prep_block_sum(sum);
-    if (threadIdx.x == 0) {
-        const double d = sqrt(sum) + L.eps;
-        int e = 0;
-        if (isfinite(d) && d > 0.0) e = -ilogb(d);
-        e = e < -100 ? -100 : e > 100 ? 100 : e;
-        g.scale[slot] = make_float2(static_cast<float>(scalbn(1.0, e)),
-                                    static_cast<float>(static_cast<double>(kNsScaleX) / scalbn(d, e)));
-    }
+    if (threadIdx.x == 0) g.scale[slot] = ns_scale_of(sum, L.eps);
 }
 
 __global__ void __launch_bounds__(kPrepThreads) zr_ns_start_kernel(const __grid_constant__ PrepLaunch L) {
@@ -1154,11 +914,13 @@ int resident_pairs() {
     return n;
 }
 
-// 256-column tiles, or 128 where that gives the pairs an evener share: a
-// half tile costs a little over half a tile.
-int pick_columns(int64_t tiles256, int64_t tiles128, int64_t pairs) {
+// 256-column tiles, or 128 where that gives the pairs an evener share.  In
+// cycles: 64 contraction indices take a pair 620 or 413 (each SM takes in
+// some 55 bytes per clock), what follows a wave's products some 7000 or 5000.
+int pick_columns(int64_t tiles256, int64_t tiles128, int64_t pairs, int64_t k) {
     const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
-    return 0.55 * static_cast<double>(waves128) < static_cast<double>(waves256) ? 128 : 256;
+    const int64_t blocks = (k + kBK - 1) / kBK;
+    return waves128 * blocks * 413 + 5000 < waves256 * blocks * 620 + 7000 ? 128 : 256;
 }
 
 template <int NG, bool APPLY>
@@ -1166,14 +928,10 @@ int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float 
                    uint32_t* gave_up, void* stream) {
     const int most = resident_pairs<NG, APPLY>();
     if (most == 0) return cudaErrorLaunchOutOfResources;
-    const float a = coeffs[0], b = coeffs[1], c = coeffs[2];
     IterLaunch<NG> L{};
     L.n_groups = n;
     L.steps = steps;
-    L.k[kGram] = {kNsScaleA / (kNsScaleX * kNsScaleX), 0.0f, 0.0f};
-    L.k[kPoly] = {c * (kNsScaleB / (kNsScaleA * kNsScaleA)), b * (kNsScaleB / kNsScaleA), c * kNsScaleB};
-    L.k[kUpdate] = {1.0f / kNsScaleB, a, 1.0f};
-    L.k[3] = {1.0f / (kNsScaleB * kNsScaleX), a / kNsScaleX, 1.0f / kNsScaleX};
+    ns_factors(L.k, coeffs);
     L.decay = apply.decay;
     L.abort_word = groups[0].done + groups[0].batch;
     L.gave_up = gave_up;
@@ -1181,14 +939,18 @@ int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float 
     L.param_out = apply.param_out;
     L.targets = apply.targets;
     L.n_targets = apply.n_targets;
-    int64_t sym[2] = {0, 0}, out[2] = {0, 0};
+    int64_t sym[2] = {0, 0}, out[2] = {0, 0}, k_sym = 0, k_out = 0;
     for (int32_t i = 0; i < n; ++i)
         for (int h = 0; h < 2; ++h) {
             sym[h] += groups[i].batch * symmetric_tiles(groups[i].gram_dim(), kBN >> h);
             out[h] += groups[i].batch * full_tiles(groups[i].m, groups[i].n, kBN >> h);
         }
-    L.sym_bn = pick_columns(sym[0], sym[1], most);
-    L.out_bn = pick_columns(out[0], out[1], most);
+    for (int32_t i = 0; i < n; ++i) {
+        k_sym = std::max(k_sym, std::max(groups[i].m, groups[i].n));
+        k_out = std::max(k_out, groups[i].gram_dim());
+    }
+    L.sym_bn = pick_columns(sym[0], sym[1], most, k_sym);
+    L.out_bn = pick_columns(out[0], out[1], most, k_out);
     for (int32_t i = 0; i < n; ++i) {
         const NsGroup& s = groups[i];
         IterGroup& g = L.g[i];

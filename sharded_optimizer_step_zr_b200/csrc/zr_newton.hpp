@@ -85,6 +85,12 @@ int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* 
 // set to 1 if a wait inside a kernel ran out.
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
                          const NsApply& apply, uint32_t* gave_up, void* stream);
+// The same from the sources alone, in clusters that keep a matrix on the chip:
+// for groups whose smaller extents are at most 128 and whose larger ones fit
+// a cluster (ns_small says whether).  Nothing of the scratch is used.
+bool ns_small(const NsGroup* groups, int32_t n_groups, bool apply);
+int launch_ns_small(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
+                    const NsApply& apply, uint32_t* gave_up, void* stream);
 // Whether the fp16 range of the scratch holds every iterate that the
 // coefficients produce from singular values in [0, 1].
 bool ns_coefficients_fit(const float coeffs[3], int32_t steps);
