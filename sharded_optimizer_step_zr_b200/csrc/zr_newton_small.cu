@@ -101,10 +101,23 @@ __device__ __forceinline__ void st_cluster8(uint32_t addr, uint32_t x, uint32_t 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
-__device__ __forceinline__ float load_source(const void* p, int32_t dtype, int64_t i) {
-    if (dtype == ZR_DTYPE_F32) return static_cast<const float*>(p)[i];
-    const uint16_t u = static_cast<const uint16_t*>(p)[i];
-    return dtype == ZR_DTYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : half_value(u);
+// N elements at src + i0 + k * step, of which those with ok(k) exist; zeros
+// elsewhere.  All loads are issued before the first is used.
+template <int N, typename At, typename Ok>
+__device__ __forceinline__ void load_source(const void* src, int32_t dtype, float (&v)[N], At at, Ok ok) {
+    if (dtype == ZR_DTYPE_F32) {
+        const float* p = static_cast<const float*>(src);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = ok(k) ? __ldg(p + at(k)) : 0.0f;
+        return;
+    }
+    const uint16_t* p = static_cast<const uint16_t*>(src);
+    uint16_t u[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) u[k] = ok(k) ? __ldg(p + at(k)) : static_cast<uint16_t>(0);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k] = dtype == ZR_DTYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(u[k]) << 16) : half_value(u[k]);
 }
 // 16-byte piece j of row r of the fp32 exchange buffer (512 bytes a row).
 __device__ __forceinline__ uint32_t ex_piece(uint32_t ex, int r, int j) { return ex + r * 512 + ((j ^ (r & 7)) << 4); }
@@ -112,6 +125,48 @@ __device__ __forceinline__ uint32_t ex_piece(uint32_t ex, int r, int j) { return
 // fp32 accumulators, fp16 operands, op2's major, N / 8, M / 16
 __device__ __forceinline__ uint32_t small_idesc(uint32_t mn2, int n) {
     return (1u << 4) | (mn2 << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((kDim >> 4) << 24);
+}
+
+// This CTA's 128 / C rows of A from the cluster's partial sums, added in the
+// order of the CTAs, into every CTA's operand and diagonal.  A thread has
+// 16 / C pieces of four columns, so 16 loads in flight for any C.
+template <int C>
+__device__ __forceinline__ void exchange(uint32_t smem, int rank, int tid, float alpha) {
+    constexpr int kPieces = 16 / C;
+    uint32_t at[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) at[c] = cluster_address(smem, c);
+    const int r0 = rank * (kDim / C) + (tid >> 5), j = tid & 31;
+    float4 p[kPieces][C];
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e)
+#pragma unroll
+        for (int c = 0; c < C; ++c) p[e][c] = ld_cluster16(at[c] + ex_piece(kOffEx, r0 + 8 * e, j));
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+        const int r = r0 + 8 * e;
+        float4 s = p[e][0];
+#pragma unroll
+        for (int c = 1; c < C; ++c) {
+            s.x += p[e][c].x; s.y += p[e][c].y; s.z += p[e][c].z; s.w += p[e][c].w;
+        }
+        float v[4] = {s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha};
+        float on = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * j + i == r) {
+                on = v[i] * (1.0f / kNsScaleA);
+                v[i] = 0.0f;
+            }
+        const uint32_t to = staged(kOffA + (j >> 4) * kChunkBytes, r, (j & 15) >> 1) + 8 * (j & 1);
+        const uint32_t w0 = half2_bits(v[0], v[1]), w1 = half2_bits(v[2], v[3]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) st_cluster8(at[c] + to, w0, w1);
+        if ((r >> 2) == j) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) st_cluster_f32(at[c] + kOffDiagA + 4 * r, on);
+        }
+    }
 }
 
 template <bool APPLY>
@@ -158,28 +213,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
     if (g.tall) {
         // Z's rows run along the source's rows: lanes read side by side
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            float v[2];
+        for (int q = 0; q < 2; ++q) {
+            float v[64];
+            const int32_t c0 = col0 + half * 128 + 64 * q;
+            const int64_t e0 = src0 + static_cast<int64_t>(c0) * g.src_row + row;
+            const int32_t count = 64 * q < mine && row < g.g ? g.l - c0 : 0;
+            load_source(g.src, g.dtype, v, [&](int k) { return e0 + k * g.src_row; }, [&](int k) { return k < count; });
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int32_t c = col0 + half * 128 + 2 * i + j;
-                v[j] = 2 * i < mine && row < g.g && c < g.l ? load_source(g.src, g.dtype, src0 + c * g.src_row + row) : 0.0f;
-            }
-            x[i] = pack2(v[0], v[1]);
+            for (int i = 0; i < 32; ++i) x[32 * q + i] = pack2(v[2 * i], v[2 * i + 1]);
         }
     } else {
 #pragma unroll 1
         for (int pass = 0; pass * 128 < width; ++pass) {
             // warp w reads rows w, w + 8, ..: 32 lanes along a row
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int r = warp + 8 * i;
+            const int32_t c0 = col0 + pass * 128 + lane;
+            const int64_t e0 = src0 + warp * g.src_row + c0;
+            float v[64];
+            load_source(
+                g.src, g.dtype, v, [&](int k) { return e0 + 8 * (k >> 2) * g.src_row + 32 * (k & 3); },
+                [&](int k) { return warp + 8 * (k >> 2) < g.g && c0 + 32 * (k & 3) < g.l; });
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t cl = 32 * j + lane, c = col0 + pass * 128 + cl;
-                    const float v = r < g.g && c < g.l ? load_source(g.src, g.dtype, src0 + r * g.src_row + c) : 0.0f;
-                    st_shared_f32(ex_piece(ex, r, cl >> 2) + 4 * (cl & 3), v);
-                }
+            for (int k = 0; k < 64; ++k) {
+                const int cl = 32 * (k & 3) + lane;
+                st_shared_f32(ex_piece(ex, warp + 8 * (k >> 2), cl >> 2) + 4 * (cl & 3), v[k]);
             }
             __syncthreads();
             if (half == pass) {
@@ -204,13 +260,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
     }
 
     // The norm: squares are exact in fp64, the order of the sum is fixed.
-    double sum = 0.0;
+    double part[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
         const float2 f = unpack2(x[i]);
-        sum += static_cast<double>(f.x) * static_cast<double>(f.x);
-        sum += static_cast<double>(f.y) * static_cast<double>(f.y);
+        part[2 * (i & 1)] = fma(static_cast<double>(f.x), static_cast<double>(f.x), part[2 * (i & 1)]);
+        part[2 * (i & 1) + 1] = fma(static_cast<double>(f.y), static_cast<double>(f.y), part[2 * (i & 1) + 1]);
     }
+    double sum = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_down_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) s_sums[warp] = sum;
@@ -320,31 +377,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
                     }
                 }
                 cluster_sync();
-                // this CTA's rows: 32 pieces of four columns each
-                const int32_t rows = kDim / C;
-                for (int32_t e = tid; e < rows * 32; e += kSmallThreads) {
-                    const int r = rank * rows + (e >> 5), j = e & 31;
-                    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int32_t c = 0; c < C; ++c) {
-                        const float4 p = ld_cluster16(cluster_address(ex_piece(ex, r, j), c));
-                        s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
-                    }
-                    float v[4] = {s.x * k.alpha, s.y * k.alpha, s.z * k.alpha, s.w * k.alpha};
-                    float on = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * j + i == r) {
-                            on = v[i] * (1.0f / kNsScaleA);
-                            v[i] = 0.0f;
-                        }
-                    const uint32_t at = staged(as + (j >> 4) * kChunkBytes, r, (j & 15) >> 1) + 8 * (j & 1);
-                    const uint32_t w0 = half2_bits(v[0], v[1]), w1 = half2_bits(v[2], v[3]);
-                    for (int32_t c = 0; c < C; ++c) {
-                        st_cluster8(cluster_address(at, c), w0, w1);
-                        if ((r >> 2) == j) st_cluster_f32(cluster_address(diag_a + 4 * r, c), on);
-                    }
-                }
+                if (C == 2) exchange<2>(smem, rank, tid, k.alpha);
+                else if (C == 4) exchange<4>(smem, rank, tid, k.alpha);
+                else if (C == 8) exchange<8>(smem, rank, tid, k.alpha);
+                else exchange<16>(smem, rank, tid, k.alpha);
                 cluster_sync();
             }
         }
@@ -411,30 +447,47 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
     }
 
     // The result: element (r, c) of Z is (r, c) of X, or (c, r) for tall ones.
-    auto store = [&](int32_t r, int32_t c, float o) {
-        const int64_t i = g.tall ? c : r, j = g.tall ? r : c;
+    // N values for the elements first + at(k) of the destination.
+    const int64_t pitch = APPLY ? g.n : g.out_row;
+    auto store = [&](auto& v, int64_t first, auto at, auto ok) {
+        constexpr int N = sizeof(v) / sizeof(float);
         if constexpr (APPLY) {
-            const int64_t e = i * g.n + j;
-            float* pm = L.master + g.master_offsets[slot] + e;
-            const float q = __fsub_rn(__fmul_rn(*pm, L.decay), __fmul_rn(o, g.step_size));
-            *pm = q;
-            const uint16_t u = bf16_bits(q);
-            const int64_t po = g.param_offsets[slot] + e;
-            if (L.n_targets == 0) L.param_out[po] = u;
-            else
-                for (int t = 0; t < L.n_targets; ++t) L.targets[t][po] = u;
+            float* pm = L.master + g.master_offsets[slot] + first;
+            const int64_t po = g.param_offsets[slot] + first;
+            float p[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (ok(k)) p[k] = pm[at(k)];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (!ok(k)) continue;
+                const float q = __fsub_rn(__fmul_rn(p[k], L.decay), __fmul_rn(v[k], g.step_size));
+                pm[at(k)] = q;
+                const uint16_t u = bf16_bits(q);
+                if (L.n_targets == 0) L.param_out[po + at(k)] = u;
+                else
+                    for (int t = 0; t < L.n_targets; ++t) L.targets[t][po + at(k)] = u;
+            }
         } else {
-            g.out[slot * g.out_batch + i * g.out_row + j] = bf16_bits(o);
+            uint16_t* out = g.out + slot * g.out_batch + first;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (ok(k)) out[at(k)] = bf16_bits(v[k]);
         }
     };
     if (g.tall) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            const float2 f = unpack2(x[i]);
-            const int32_t c = col0 + half * 128 + 2 * i;
-            if (2 * i >= mine || row >= g.g) continue;
-            if (c < g.l) store(row, c, f.x);
-            if (c + 1 < g.l) store(row, c + 1, f.y);
+        for (int q = 0; q < 4; ++q) {
+            const int32_t c0 = col0 + half * 128 + 32 * q;
+            const int32_t count = 32 * q < mine && row < g.g ? g.l - c0 : 0;
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = unpack2(x[16 * q + i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+            store(v, c0 * pitch + row, [&](int k) { return k * pitch; }, [&](int k) { return k < count; });
         }
     } else {
 #pragma unroll 1
@@ -449,15 +502,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
                 }
             }
             __syncthreads();
-            const int32_t cols = min(width - pass * 128, 128);
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int r = warp + 8 * i;
+            // 32 lanes along a row; columns past the width are the next CTA's
+            const int32_t cols = min(min(width - pass * 128, 128), g.l - (col0 + pass * 128));
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int r0 = warp + 64 * i;
+                float v[32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t cl = 32 * j + lane, c = col0 + pass * 128 + cl;
-                    if (r < g.g && cl < cols && c < g.l) store(r, c, ld_shared_f32(ex_piece(ex, r, cl >> 2) + 4 * (cl & 3)));
+                for (int k = 0; k < 32; ++k) {
+                    const int cl = 32 * (k & 3) + lane;
+                    v[k] = ld_shared_f32(ex_piece(ex, r0 + 8 * (k >> 2), cl >> 2) + 4 * (cl & 3));
                 }
+                store(v, r0 * pitch + col0 + pass * 128 + lane, [&](int k) { return 8 * (k >> 2) * pitch + 32 * (k & 3); },
+                      [&](int k) { return r0 + 8 * (k >> 2) < g.g && 32 * (k & 3) + lane < cols; });
             }
         }
     }
