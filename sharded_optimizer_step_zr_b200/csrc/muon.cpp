@@ -53,7 +53,7 @@ struct zr_muon {
     std::vector<int64_t> owned_offsets, global_offsets;   // per matrix
 
     // workspace regions
-    uint64_t at_status = 0, at_tiles = 0, at_first = 0, at_owned = 0, at_global = 0, at_scale = 0, at_partials = 0,
+    uint64_t at_status = 0, at_tiles = 0, at_first = 0, at_owned = 0, at_global = 0, at_scale = 0, at_partials = 0, at_maps = 0,
              total = 0;
     std::vector<uint64_t> at_group;
 
@@ -77,6 +77,7 @@ void lay_out(zr_muon& u) {
     take(u.at_global, sizeof(int64_t) * n);
     take(u.at_scale, sizeof(float2) * n);
     take(u.at_partials, sizeof(double) * u.tiles.size());
+    take(u.at_maps, zr::ns_maps_bytes(static_cast<int32_t>(u.groups.size())));
     u.at_group.clear();
     for (const zr::NsGroup& g : u.groups) {
         uint64_t at;
@@ -257,16 +258,15 @@ zr_status zr_orthogonalize(const void* x, int32_t dtype, int64_t batch, int64_t 
     const uint64_t at_partials = 256 + align256(sizeof(float2) * static_cast<uint64_t>(batch));
     g.n_partials = static_cast<int32_t>(zr::ns_partials_per_matrix(m, n));
     g.partials = reinterpret_cast<double*>(base + at_partials);
-    if (zr::ns_bind_scratch(g, base + need - zr::ns_scratch_bytes(batch, m, n)) != cudaSuccess) return ZR_ERR_CUDA;
-    if (cudaMemsetAsync(base, 0, sizeof(uint32_t), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return ZR_ERR_CUDA;
     const float coeffs[3] = {ns->a, ns->b, ns->c};
     uint32_t* gave_up = reinterpret_cast<uint32_t*>(base);
     if (zr::ns_small(&g, 1, false))
-        return cuda_status(zr::launch_ns_small(&g, 1, ns->steps, coeffs, ns->eps, zr::NsApply(), gave_up, stream));
-    int e = zr::launch_ns_sumsq(&g, 1, stream);
+        return cuda_status(zr::launch_ns_small(&g, 1, ns->steps, coeffs, ns->eps, zr::NsApply(), gave_up, true,
+                                              stream));
+    if (zr::ns_bind_scratch(g, base + need - zr::ns_scratch_bytes(batch, m, n)) != cudaSuccess) return ZR_ERR_CUDA;
+    int e = zr::launch_ns_sumsq(g, gave_up, stream);
     if (e == cudaSuccess) e = zr::launch_ns_scales(&g, 1, ns->eps, stream);
-    if (e == cudaSuccess) e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, zr::NsApply(), gave_up, stream);
+    if (e == cudaSuccess) e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, zr::NsApply(), nullptr, gave_up, stream);
     return cuda_status(e);
 }
 
@@ -351,6 +351,15 @@ zr_status zr_muon_set_workspace(zr_muon* u, void* d_ws, uint64_t bytes, zr_strea
         g.master_offsets = reinterpret_cast<const int64_t*>(base + u->at_owned) + first;
         first += g.batch;
     }
+    std::vector<char> maps;
+    try {
+        maps.resize(zr::ns_maps_bytes(static_cast<int32_t>(u->groups.size())));
+    } catch (...) {
+        return ZR_ERR_INVALID_ARG;
+    }
+    if (!maps.empty() && (zr::ns_fill_maps(u->groups.data(), static_cast<int32_t>(u->groups.size()), maps.data()) != cudaSuccess ||
+                          !up(u->at_maps, maps.data(), maps.size())))
+        return ZR_ERR_CUDA;
     u->device = dev;
     u->d_workspace = base;
     return ZR_OK;
@@ -408,10 +417,12 @@ zr_status zr_muon_step(const zr_muon* u, const void* const* grad_ptrs, float* ma
     // Small matrices beside large ones cost the persistent kernel nothing:
     // they run while the large ones' products wait for one another.
     if (zr::ns_small(groups.data(), n, true))
-        return cuda_status(zr::launch_ns_small(groups.data(), n, u->hp.ns.steps, coeffs, u->hp.ns.eps, apply, gave_up, stream));
+        return cuda_status(zr::launch_ns_small(groups.data(), n, u->hp.ns.steps, coeffs, u->hp.ns.eps, apply, gave_up,
+                                              false, stream));
     e = zr::launch_ns_scales(groups.data(), n, u->hp.ns.eps, stream);
     if (e == cudaSuccess)
-        e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, apply, gave_up, stream);
+        e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, apply, u->d_workspace + u->at_maps, gave_up,
+                                     stream);
     return cuda_status(e);
 }
 

@@ -34,6 +34,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "zr.h"
 #include "zr_newton.hpp"
@@ -63,18 +64,18 @@ constexpr int kSmemBars = kSmemDiag + kEpiWarps * kDiagBytes;
 constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
 constexpr int kIterSmem = kSmemBars + 8 * kBars + 16;
 static_assert(kIterSmem <= 227 * 1024, "one CTA per SM");
-constexpr int kMaxGroups = 12;                             // of a launch: its parameters stay below 32 KB
+constexpr int kMaxGroups = 16;                             // of a launch
 
 enum : int { kGram = 0, kPoly = 1, kUpdate = 2 };          // products of a step, in order
 
-// Tensor maps of the products' operands; pairs are for either X.
-struct IterOperands {
+// A group's tensor maps: the products' operands (pairs are for either X), and
+// the epilogue's, as in NsMaps.
+struct IterMaps {
     CUtensorMap gram1[2], gram2[2], poly1, poly2, update1[2], update2[2];
+    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;
 };
 
 struct IterGroup {
-    IterOperands op;
-    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;    // as in NsMaps
     int32_t m, n, dim, tall;
     int32_t sym_tiles, out_tiles, out_tiles_n;             // tiles of a matrix: A and A A; the update
     int64_t first_sym, first_out;                          // the group's first tile of a product
@@ -87,8 +88,20 @@ struct IterGroup {
     float step_size;
 };
 
+// Parameters past 4 KB cost a launch 70 us on the host, so only a single
+// group's maps are among them; those of several are in device memory.
+struct InlineMaps {
+    IterMaps one;
+    __device__ __forceinline__ const IterMaps& of(int32_t) const { return one; }
+};
+struct DeviceMaps {
+    const IterMaps* all;
+    __device__ __forceinline__ const IterMaps& of(int32_t group) const { return all[group]; }
+};
 template <int NG>
 struct IterLaunch {
+    std::conditional_t<NG == 1, InlineMaps, DeviceMaps> maps;
+    IterGroup g[NG];
     int32_t n_groups, steps, pairs;
     int32_t sym_bn, out_bn;
     int64_t sym_total, out_total;                          // tiles of all matrices
@@ -99,8 +112,9 @@ struct IterLaunch {
     uint16_t* param_out;
     uint16_t* const* targets;
     int32_t n_targets;
-    IterGroup g[NG];
 };
+static_assert(sizeof(IterLaunch<1>) <= 4096 && sizeof(IterLaunch<kMaxGroups>) <= 4096, "a launch's fast parameters");
+
 
 // ---------------------------------------------------------------------------
 // tiles
@@ -249,9 +263,10 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 }
                 s_ready = ++seen;
                 const int from = at.step & 1;
+                const IterMaps& maps = L.maps.of(at.group);
                 const bool mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
-                const CUtensorMap* op1 = at.op == kGram ? &g.op.gram1[from] : at.op == kPoly ? &g.op.poly1 : &g.op.update1[from];
-                const CUtensorMap* op2 = at.op == kGram ? &g.op.gram2[from] : at.op == kPoly ? &g.op.poly2 : &g.op.update2[from];
+                const CUtensorMap* op1 = at.op == kGram ? &maps.gram1[from] : at.op == kPoly ? &maps.poly1 : &maps.update1[from];
+                const CUtensorMap* op2 = at.op == kGram ? &maps.gram2[from] : at.op == kPoly ? &maps.poly2 : &maps.update2[from];
                 const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
                 const int32_t nk = (k + kBK - 1) / kBK;
                 // A box of a K-major operand is 64 contraction indices x 64 or
@@ -329,8 +344,9 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             const int32_t row_w = at.row0 + rank * 128 + quad * 32, row = row_w + lane;
             const int32_t chunks = row_w < rows ? (min(at.bn, cols - at.col0) + 63) / 64 : 0;
             const uint32_t buf = acc & 1;
-            const CUtensorMap* in_hi = at.op == kPoly ? &g.egram : &g.exh[at.step & 1];
-            const CUtensorMap* in_lo = &g.exl[at.step & 1];
+            const IterMaps& maps = L.maps.of(at.group);
+            const CUtensorMap* in_hi = at.op == kPoly ? &maps.egram : &maps.exh[at.step & 1];
+            const CUtensorMap* in_lo = &maps.exl[at.step & 1];
             auto load = [&](int ch) {              // lane 0: the elementwise operand of a chunk
                 const int32_t x = at.col0 + ch * 64;
                 mbar_expect(in_bar, sym ? kPartBytes : 2 * kPartBytes);
@@ -496,12 +512,12 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     __syncwarp();
                     if (lane == 0) {
                         if (sym) {
-                            tma_store(at.op == kGram ? &g.egram : &g.epoly, c, row_w, at.slot, hi);
+                            tma_store(at.op == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
                             if (mirror)
-                                tma_store(at.op == kGram ? &g.mgram : &g.mpoly, row_w, c, at.slot, lo);
+                                tma_store(at.op == kGram ? &maps.mgram : &maps.mpoly, row_w, c, at.slot, lo);
                         } else {
-                            tma_store(&g.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
-                            tma_store(&g.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
+                            tma_store(&maps.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
+                            tma_store(&maps.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
                         }
                         store_commit();
                         if (at.op != kGram && ch + 2 < chunks) {
@@ -671,7 +687,7 @@ struct PrepGroup {
 };
 struct PrepLaunch {
     int32_t n_groups;
-    uint32_t* abort_word;
+    uint32_t *abort_word, *gave_up;
     int32_t total_matrices;
     double eps;
     PrepGroup g[kMaxGroups];
@@ -756,6 +772,7 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_sumsq_kernel(const __grid_
         }
     }
     sum = prep_block_sum(sum);
+    if (threadIdx.x == 0 && blockIdx.x == 0 && L.gave_up) *L.gave_up = 0u;
     if (threadIdx.x == 0) g.partials[static_cast<int64_t>(at.slot) * g.n_partials + at.piece] = sum;
 }
 
@@ -923,15 +940,53 @@ int pick_columns(int64_t tiles256, int64_t tiles128, int64_t pairs, int64_t k) {
     return waves128 * blocks * 413 + 5000 < waves256 * blocks * 620 + 7000 ? 128 : 256;
 }
 
+struct Tiling { int sym_bn, out_bn; };
+Tiling tiling(const NsGroup* groups, int32_t n, int64_t pairs) {
+    int64_t sym[2] = {0, 0}, out[2] = {0, 0}, k_sym = 0, k_out = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        for (int h = 0; h < 2; ++h) {
+            sym[h] += groups[i].batch * symmetric_tiles(groups[i].gram_dim(), kBN >> h);
+            out[h] += groups[i].batch * full_tiles(groups[i].m, groups[i].n, kBN >> h);
+        }
+        k_sym = std::max(k_sym, std::max(groups[i].m, groups[i].n));
+        k_out = std::max(k_out, groups[i].gram_dim());
+    }
+    return {pick_columns(sym[0], sym[1], pairs, k_sym), pick_columns(out[0], out[1], pairs, k_out)};
+}
+
+void fill_maps(IterMaps& o, const NsGroup& s, Tiling t) {
+    const NsMaps& m = s.maps;
+    const bool sym_half = t.sym_bn != kBN, out_half = t.out_bn != kBN, tall = s.m > s.n;
+    for (int j = 0; j < 2; ++j) {
+        o.gram1[j] = tall ? m.x_chunks[j] : m.x_rows[j];
+        o.gram2[j] = sym_half ? m.x_box[j] : o.gram1[j];
+        o.update1[j] = tall ? m.x_rows[j] : m.poly_rows;
+        o.update2[j] = tall ? (out_half ? m.poly_box : m.poly_rows) : out_half ? m.x_box[j] : m.x_chunks[j];
+        o.exh[j] = m.exh[j];
+        o.exl[j] = m.exl[j];
+    }
+    o.poly1 = m.gram_rows;
+    o.poly2 = sym_half ? m.gram_box : m.gram_rows;
+    o.egram = m.egram;
+    o.epoly = m.epoly;
+    o.mgram = m.mgram;
+    o.mpoly = m.mpoly;
+}
+
 template <int NG, bool APPLY>
-int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float coeffs[3], const NsApply& apply,
-                   uint32_t* gave_up, void* stream) {
+int launch_iterate(const NsGroup* groups, int32_t n, const IterMaps* maps, int32_t steps, const float coeffs[3],
+                   const NsApply& apply, uint32_t* gave_up, void* stream) {
     const int most = resident_pairs<NG, APPLY>();
     if (most == 0) return cudaErrorLaunchOutOfResources;
     IterLaunch<NG> L{};
     L.n_groups = n;
     L.steps = steps;
     ns_factors(L.k, coeffs);
+    const Tiling t = tiling(groups, n, resident_pairs<NG, APPLY>());
+    L.sym_bn = t.sym_bn;
+    L.out_bn = t.out_bn;
+    if constexpr (NG == 1) fill_maps(L.maps.one, groups[0], t);
+    else L.maps.all = maps;
     L.decay = apply.decay;
     L.abort_word = groups[0].done + groups[0].batch;
     L.gave_up = gave_up;
@@ -939,37 +994,9 @@ int launch_iterate(const NsGroup* groups, int32_t n, int32_t steps, const float 
     L.param_out = apply.param_out;
     L.targets = apply.targets;
     L.n_targets = apply.n_targets;
-    int64_t sym[2] = {0, 0}, out[2] = {0, 0}, k_sym = 0, k_out = 0;
-    for (int32_t i = 0; i < n; ++i)
-        for (int h = 0; h < 2; ++h) {
-            sym[h] += groups[i].batch * symmetric_tiles(groups[i].gram_dim(), kBN >> h);
-            out[h] += groups[i].batch * full_tiles(groups[i].m, groups[i].n, kBN >> h);
-        }
-    for (int32_t i = 0; i < n; ++i) {
-        k_sym = std::max(k_sym, std::max(groups[i].m, groups[i].n));
-        k_out = std::max(k_out, groups[i].gram_dim());
-    }
-    L.sym_bn = pick_columns(sym[0], sym[1], most, k_sym);
-    L.out_bn = pick_columns(out[0], out[1], most, k_out);
     for (int32_t i = 0; i < n; ++i) {
         const NsGroup& s = groups[i];
         IterGroup& g = L.g[i];
-        const NsMaps& t = s.maps;
-        const bool sym_half = L.sym_bn != kBN, out_half = L.out_bn != kBN, tall = s.m > s.n;
-        for (int j = 0; j < 2; ++j) {
-            g.op.gram1[j] = tall ? t.x_chunks[j] : t.x_rows[j];
-            g.op.gram2[j] = sym_half ? t.x_box[j] : g.op.gram1[j];
-            g.op.update1[j] = tall ? t.x_rows[j] : t.poly_rows;
-            g.op.update2[j] = tall ? (out_half ? t.poly_box : t.poly_rows) : out_half ? t.x_box[j] : t.x_chunks[j];
-            g.exh[j] = t.exh[j];
-            g.exl[j] = t.exl[j];
-        }
-        g.op.poly1 = t.gram_rows;
-        g.op.poly2 = sym_half ? t.gram_box : t.gram_rows;
-        g.egram = t.egram;
-        g.epoly = t.epoly;
-        g.mgram = t.mgram;
-        g.mpoly = t.mpoly;
         g.m = static_cast<int32_t>(s.m);
         g.n = static_cast<int32_t>(s.n);
         g.dim = static_cast<int32_t>(s.gram_dim());
@@ -1116,16 +1143,13 @@ int ns_bind_scratch(NsGroup& g, void* base) {
     return e;
 }
 
-int launch_ns_sumsq(const NsGroup* groups, int32_t n_groups, void* stream) {
-    for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
-        PrepLaunch L{};
-        const int64_t pieces = fill_prep(L, groups + at, std::min(kMaxGroups, n_groups - at));
-        if (pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
-        Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
-        const cudaError_t e = d.run(zr_ns_sumsq_kernel, L);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream) {
+    PrepLaunch L{};
+    const int64_t pieces = fill_prep(L, &group, 1);
+    if (pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    L.gave_up = gave_up;
+    Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
+    return d.run(zr_ns_sumsq_kernel, L);
 }
 
 int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* stream) {
@@ -1141,7 +1165,8 @@ int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* 
 }
 
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
-                         const NsApply& apply, uint32_t* gave_up, void* stream) {
+                         const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream) {
+    const IterMaps* maps = static_cast<const IterMaps*>(device_maps);
     for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
         const NsGroup* gs = groups + at;
         const int32_t n = std::min(kMaxGroups, n_groups - at);
@@ -1152,12 +1177,30 @@ int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps,
         int e = d.run(zr_ns_start_kernel, P);
         if (e != cudaSuccess) return e;
         if (apply.master)
-            e = n == 1 ? launch_iterate<1, true>(gs, n, steps, coeffs, apply, gave_up, stream)
-                       : launch_iterate<kMaxGroups, true>(gs, n, steps, coeffs, apply, gave_up, stream);
+            e = n == 1 ? launch_iterate<1, true>(gs, n, nullptr, steps, coeffs, apply, gave_up, stream)
+                       : launch_iterate<kMaxGroups, true>(gs, n, maps + at, steps, coeffs, apply, gave_up, stream);
         else
-            e = n == 1 ? launch_iterate<1, false>(gs, n, steps, coeffs, apply, gave_up, stream)
-                       : launch_iterate<kMaxGroups, false>(gs, n, steps, coeffs, apply, gave_up, stream);
+            e = n == 1 ? launch_iterate<1, false>(gs, n, nullptr, steps, coeffs, apply, gave_up, stream)
+                       : launch_iterate<kMaxGroups, false>(gs, n, maps + at, steps, coeffs, apply, gave_up, stream);
         if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+uint64_t ns_maps_bytes(int32_t n_groups) { return sizeof(IterMaps) * static_cast<uint64_t>(n_groups); }
+
+int ns_fill_maps(const NsGroup* groups, int32_t n_groups, void* host) {
+    const int pairs = resident_pairs<kMaxGroups, true>();
+    if (pairs == 0) return cudaErrorLaunchOutOfResources;
+    char* to = static_cast<char*>(host);          // of any alignment
+    for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
+        const int32_t n = std::min(kMaxGroups, n_groups - at);
+        const Tiling t = tiling(groups + at, n, pairs);
+        for (int32_t i = 0; i < n; ++i) {
+            IterMaps maps;
+            fill_maps(maps, groups[at + i], t);
+            std::memcpy(to + sizeof maps * static_cast<size_t>(at + i), &maps, sizeof maps);
+        }
     }
     return cudaSuccess;
 }

@@ -77,20 +77,26 @@ int ns_bind_scratch(NsGroup& g, void* base);
 // How many partial sums of squares launch_ns_sumsq writes for one matrix.
 int64_t ns_partials_per_matrix(int64_t m, int64_t n);
 
-// Sums of squares of every source matrix into partials (one CTA per piece).
-int launch_ns_sumsq(const NsGroup* groups, int32_t n_groups, void* stream);
+// Sums of squares of every source matrix into partials (one CTA per piece),
+// and *gave_up cleared.
+int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream);
 // The matrices' scales 1 / (norm + eps) from the partials.
 int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* stream);
 // X_0, then `steps` iterations, then the destination.  *gave_up (device) is
 // set to 1 if a wait inside a kernel ran out.
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
-                         const NsApply& apply, uint32_t* gave_up, void* stream);
+                         const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream);
+// What several groups' launches need in device memory (device_maps; 128-byte
+// aligned), filled on the host for the current device; a single group needs none.
+uint64_t ns_maps_bytes(int32_t n_groups);
+int ns_fill_maps(const NsGroup* groups, int32_t n_groups, void* host);
 // The same from the sources alone, in clusters that keep a matrix on the chip:
 // for groups whose smaller extents are at most 128 and whose larger ones fit
-// a cluster (ns_small says whether).  Nothing of the scratch is used.
+// a cluster (ns_small says whether).  Nothing of the scratch is used.  With
+// `clear`, *gave_up is cleared first.
 bool ns_small(const NsGroup* groups, int32_t n_groups, bool apply);
 int launch_ns_small(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
-                    const NsApply& apply, uint32_t* gave_up, void* stream);
+                    const NsApply& apply, uint32_t* gave_up, bool clear, void* stream);
 // Whether the fp16 range of the scratch holds every iterate that the
 // coefficients produce from singular values in [0, 1].
 bool ns_coefficients_fit(const float coeffs[3], int32_t steps);

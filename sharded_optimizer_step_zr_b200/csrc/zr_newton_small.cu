@@ -58,6 +58,7 @@ struct SmallLaunch {
     double eps;
     float decay;
     uint32_t* gave_up;
+    int32_t clear;                              // *gave_up first
     float* master;
     uint16_t* param_out;
     uint16_t* const* targets;
@@ -127,24 +128,29 @@ __device__ __forceinline__ uint32_t small_idesc(uint32_t mn2, int n) {
     return (1u << 4) | (mn2 << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((kDim >> 4) << 24);
 }
 
-// This CTA's 128 / C rows of A from the cluster's partial sums, added in the
-// order of the CTAs, into every CTA's operand and diagonal.  A thread has
-// 16 / C pieces of four columns, so 16 loads in flight for any C.
+// Every C-th row of A from the cluster's partial sums, added in the order of
+// the CTAs, into every CTA's operand and diagonal.  A thread has 16 / C
+// pieces of four columns, so 16 loads in flight for any C.  Bound by the
+// distributed shared memory (some 18 bytes per clock): rows and columns past
+// `dim` stay as they are, zero.
 template <int C>
-__device__ __forceinline__ void exchange(uint32_t smem, int rank, int tid, float alpha) {
+__device__ __forceinline__ void exchange(uint32_t smem, int rank, int tid, int dim, float alpha) {
     constexpr int kPieces = 16 / C;
     uint32_t at[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) at[c] = cluster_address(smem, c);
-    const int r0 = rank * (kDim / C) + (tid >> 5), j = tid & 31;
+    const int j = tid & 31;
+    auto row_of = [&](int e) { return ((tid >> 5) + 8 * e) * C + rank; };
+    if (4 * j >= dim) return;
     float4 p[kPieces][C];
 #pragma unroll
     for (int e = 0; e < kPieces; ++e)
 #pragma unroll
-        for (int c = 0; c < C; ++c) p[e][c] = ld_cluster16(at[c] + ex_piece(kOffEx, r0 + 8 * e, j));
+        for (int c = 0; c < C; ++c) p[e][c] = ld_cluster16(at[c] + ex_piece(kOffEx, min(row_of(e), dim - 1), j));
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-        const int r = r0 + 8 * e;
+        const int r = row_of(e);
+        if (r >= dim) continue;
         float4 s = p[e][0];
 #pragma unroll
         for (int c = 1; c < C; ++c) {
@@ -206,6 +212,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
     const int32_t mine = min(max(width - half * 128, 0), 128);  // of them, in this warp's half (a multiple of 64)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (a wait gives up 20 s after its block began: never before block 0 is here)
+    if (blockIdx.x == 0 && tid == 0 && L.clear) *L.gave_up = 0u;
 
     // Z, a row's 128 columns per thread: x[i] holds columns 2 i and 2 i + 1.
     f32x2 x[64];
@@ -340,6 +348,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
     };
     const bool on_diagonal = half == (quad >> 1);    // this warp's 64 columns of A hold its rows' diagonal
 
+    if (C > 1) {
+        for (int i = tid; i < 2 * kChunkBytes / 16; i += kSmallThreads) st_shared16(as + 16 * i, make_uint4(0, 0, 0, 0));
+        if (tid < kDim) st_shared_f32(diag_a + 4 * tid, 0.0f);
+    }
     write_operand();
 #pragma unroll 1
     for (int32_t step = 0; step < L.steps; ++step) {
@@ -377,10 +389,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
                     }
                 }
                 cluster_sync();
-                if (C == 2) exchange<2>(smem, rank, tid, k.alpha);
-                else if (C == 4) exchange<4>(smem, rank, tid, k.alpha);
-                else if (C == 8) exchange<8>(smem, rank, tid, k.alpha);
-                else exchange<16>(smem, rank, tid, k.alpha);
+                if (C == 2) exchange<2>(smem, rank, tid, g.g, k.alpha);
+                else if (C == 4) exchange<4>(smem, rank, tid, g.g, k.alpha);
+                else if (C == 8) exchange<8>(smem, rank, tid, g.g, k.alpha);
+                else exchange<16>(smem, rank, tid, g.g, k.alpha);
                 cluster_sync();
             }
         }
@@ -563,7 +575,7 @@ bool clusters_run(int ctas) {
 
 template <bool APPLY>
 int launch_small(const NsGroup* groups, int32_t n, int ctas, int32_t steps, const float coeffs[3], double eps,
-                 const NsApply& apply, uint32_t* gave_up, void* stream) {
+                 const NsApply& apply, uint32_t* gave_up, bool clear, void* stream) {
     SmallLaunch L{};
     L.n_groups = n;
     L.steps = steps;
@@ -572,6 +584,7 @@ int launch_small(const NsGroup* groups, int32_t n, int ctas, int32_t steps, cons
     L.eps = eps;
     L.decay = apply.decay;
     L.gave_up = gave_up;
+    L.clear = clear;
     L.master = apply.master;
     L.param_out = apply.param_out;
     L.targets = apply.targets;
@@ -627,13 +640,13 @@ bool ns_small(const NsGroup* groups, int32_t n_groups, bool apply) {
 }
 
 int launch_ns_small(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
-                    const NsApply& apply, uint32_t* gave_up, void* stream) {
+                    const NsApply& apply, uint32_t* gave_up, bool clear, void* stream) {
     for (int32_t at = 0; at < n_groups; at += kSmallGroups) {
         const int32_t n = std::min(kSmallGroups, n_groups - at);
         int most = 1;
         for (int32_t i = 0; i < n; ++i) most = std::max(most, cluster_ctas(std::max(groups[at + i].m, groups[at + i].n)));
-        const int e = apply.master ? launch_small<true>(groups + at, n, most, steps, coeffs, eps, apply, gave_up, stream)
-                                   : launch_small<false>(groups + at, n, most, steps, coeffs, eps, apply, gave_up, stream);
+        const int e = apply.master ? launch_small<true>(groups + at, n, most, steps, coeffs, eps, apply, gave_up, clear, stream)
+                                   : launch_small<false>(groups + at, n, most, steps, coeffs, eps, apply, gave_up, clear, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

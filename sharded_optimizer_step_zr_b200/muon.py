@@ -11,6 +11,9 @@ supplies device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
+import functools
+
 from . import (ZR_DTYPE_BF16, ZR_DTYPE_F16, ZR_DTYPE_F32, ZR_MOMENTUM_F32, ZR_MOMENTUM_INT8, ZR_MUON_SCALE_RMS,
                ZR_MUON_SCALE_SPECTRAL, zr_muon_check_result, zr_muon_create, zr_muon_dequantize_momentum,
                zr_muon_destroy, zr_muon_quantize_momentum, zr_muon_scales, zr_muon_set_params,
@@ -21,6 +24,14 @@ from .plan import _require_all
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 _SCALES = {"spectral": ZR_MUON_SCALE_SPECTRAL, "rms": ZR_MUON_SCALE_RMS}
 _FORMATS = {"f32": ZR_MOMENTUM_F32, "int8": ZR_MOMENTUM_INT8}
+_nothing = contextlib.nullcontext()
+_workspace_bytes = functools.lru_cache(maxsize=1024)(zr_orthogonalize_workspace_bytes)     # of the sizes alone
+
+
+@functools.cache
+def _dtypes():
+    import torch
+    return {torch.float32: ZR_DTYPE_F32, torch.bfloat16: ZR_DTYPE_BF16, torch.float16: ZR_DTYPE_F16}
 
 
 def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=None, stream=None):
@@ -35,25 +46,26 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     stream: a torch.cuda.Stream of x's device; by default that device's
     current one."""
     import torch
-    dtypes = {torch.float32: ZR_DTYPE_F32, torch.bfloat16: ZR_DTYPE_BF16, torch.float16: ZR_DTYPE_F16}
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"x: expected a torch tensor, got {type(x).__name__}")
-    if x.dtype not in dtypes:
+    dtype = _dtypes().get(x.dtype)
+    if dtype is None:
         raise ValueError(f"x: dtype {x.dtype}, expected float32, bfloat16 or float16")
-    if x.device.type != "cuda":
-        raise ValueError(f"x: must be on a CUDA device, is on {x.device}")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError(f"x: must be on a CUDA device, is on {device}")
     if x.dim() < 2:
         raise ValueError(f"x: {x.dim()} dimensions, expected at least 2")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=device)
         if x.shape[-1] > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or x.shape[-2] == 1):
-            out = torch.empty(x.mT.shape, dtype=torch.bfloat16, device=x.device).mT
+            out = torch.empty(x.mT.shape, dtype=torch.bfloat16, device=device).mT
     else:
         if not isinstance(out, torch.Tensor):
             raise TypeError(f"out: expected a torch tensor, got {type(out).__name__}")
-        if out.dtype != torch.bfloat16 or out.shape != x.shape or out.device != x.device:
+        if out.dtype != torch.bfloat16 or out.shape != x.shape or out.device != device:
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected torch.bfloat16 "
-                             f"{tuple(x.shape)} on {x.device}")
+                             f"{tuple(x.shape)} on {device}")
     result = out
     if x.numel() == 0:
         return result
@@ -68,29 +80,31 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
         x, out = x.mT, out.mT
     m, n = x.shape[-2:]
 
-    def batched(t, what):
-        """One batch extent: the leading ones as a single stride."""
-        try:
-            t = t.unsqueeze(0) if t.dim() == 2 else t if t.dim() == 3 else t.view(-1, m, n)
-        except RuntimeError as e:
-            raise ValueError(f"{what}: its leading extents are not one stride apart") from e
-        return t, (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if m > 1 else n)
+    def strides(t, what):
+        """Batch and row stride, the leading extents as one batch."""
+        if t.dim() > 3:
+            try:
+                t = t.view(-1, m, n)
+            except RuntimeError as e:
+                raise ValueError(f"{what}: its leading extents are not one stride apart") from e
+        return (t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else 0), (t.stride(-2) if m > 1 else n)
 
-    x, x_batch, x_row = batched(x, "x")
-    out, o_batch, o_row = batched(out, "out")
-    need = zr_orthogonalize_workspace_bytes(x.shape[0], m, n)
-    if stream is not None and not isinstance(stream, int) and stream.device != x.device:
-        raise ValueError(f"stream: of {stream.device}, x is on {x.device}")
-    with torch.cuda.device(x.device):
+    batch = x.numel() // (m * n)
+    x_batch, x_row = strides(x, "x")
+    o_batch, o_row = strides(out, "out")
+    need = _workspace_bytes(batch, m, n)
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, x is on {device}")
+    with torch.cuda.device(device) if torch.cuda.current_device() != device.index else _nothing:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
             if stream is not None:       # it is freed when this call returns, maybe before its work is done
-                s = torch.cuda.ExternalStream(stream, device=x.device) if isinstance(stream, int) else stream
+                s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
                 workspace.record_stream(s)
         else:
-            _require_all([(workspace, "workspace", torch.uint8, need, False)], x.device)
-        zr_orthogonalize(x, dtypes[x.dtype], x.shape[0], m, n, x_batch, x_row, out, o_batch, o_row, coeffs, eps,
-                         steps, workspace, workspace.numel(), stream)
+            _require_all([(workspace, "workspace", torch.uint8, need, False)], device)
+        zr_orthogonalize(x, dtype, batch, m, n, x_batch, x_row, out, o_batch, o_row, coeffs, eps, steps, workspace,
+                         workspace.numel(), stream)
     return result
 
 
