@@ -249,8 +249,9 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
     const uint32_t tmem = s_tmem;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             fence_async_global();      // the kernel before this one wrote X_0 by ordinary stores
+            const uint32_t pair_full = leader_address(full);
             uint32_t it = 0, seen = 0;
             bool ok = true;
             for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next()) {
@@ -283,7 +284,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                     const uint32_t dst = smem + s * kStageBytes;
                     if (rank == 0) mbar_expect(full + 8 * s, bytes);
-                    const uint32_t bar = leader_address(full + 8 * s);
+                    const uint32_t bar = pair_full + 8 * s;
                     const int k0 = kb * kBK;
                     if (mn1) tma_load_chunks(dst, op1, k0, r0 / 64, at.slot, bar);
                     else tma_load_pair(dst, op1, k0, r0, at.slot, bar);
@@ -293,7 +294,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             uint32_t it = 0, acc = 0;
             bool ok = true;
             for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next(), ++acc) {
@@ -335,6 +336,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
         const uint32_t in_bar = staged_in + 8 * (warp - 2);
         const uint32_t free_bar = leader_address(acc_empty);
         uint32_t in_phase = 0;                     // parity of the next load
+        const bool one = elect_one();              // the lane that issues this warp's copies
         uint32_t acc = 0;
         for (TileWalk<NG> walk(L, pair); walk.live(); walk.next(), ++acc) {
             const TileAt at = walk.at();
@@ -359,7 +361,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             float dr = 0.0f;
             if (at.op != kGram && turn < chunks) {
                 bool ok = true;
-                if (lane == 0) {
+                if (one) {
                     ok = s_ready > acc || wait_slow([&] { return s_ready > acc; }, bail);
                     if (ok) {
                         (void)ld_acquire(g.done + at.slot);
@@ -368,7 +370,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         load(turn);
                     }
                 }
-                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
                 if (by_row && row < rows) dr = __ldcg(diag + row);
             }
             const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN;
@@ -386,7 +388,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 // the products still run
                 f32x2 y[2][16];
                 if (at.op == kGram) {
-                    if (lane == 0) store_wait_read<0>();
+                    if (one) store_wait_read<0>();
                 } else {
                     if (by_col) {
                         float d[2];
@@ -461,7 +463,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     if (ch + 2 < chunks) return;
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
+                    if (one) mbar_arrive_cluster(free_bar + 8 * buf);
                 };
                 if (!last) {
 #pragma unroll
@@ -510,7 +512,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (one) {
                         if (sym) {
                             tma_store(at.op == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
                             if (mirror)
@@ -572,7 +574,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         }
                     }
                     __syncwarp();
-                    if (lane == 0 && ch + 2 < chunks) {
+                    if (one && ch + 2 < chunks) {
                         fence_async_shared();
                         load(ch + 2);
                     }
@@ -620,7 +622,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                                 }
                     }
                     __syncwarp();
-                    if (lane == 0 && ch + 2 < chunks) {
+                    if (one && ch + 2 < chunks) {
                         fence_async_shared();
                         load(ch + 2);
                     }
@@ -630,18 +632,18 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             if (turn >= chunks) {
                 if (!products()) break;
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(free_bar + 8 * buf);
+                if (one) mbar_arrive_cluster(free_bar + 8 * buf);
             }
             if (!last) {
                 __syncwarp();
-                if (lane == 0) {
+                if (one) {
                     store_wait();
                     fence_async_global();
                     red_release(g.done + at.slot, 1u);
                 }
             }
         }
-        if (lane == 0) store_wait();
+        if (one) store_wait();
     }
     // Every role is done (or gave up).  A pair that gave up may still have
     // copies and products in flight: the copies land within microseconds, and

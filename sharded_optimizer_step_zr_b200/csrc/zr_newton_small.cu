@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
         fence_async_shared();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             issue();
             mma_commit_one(bar);
