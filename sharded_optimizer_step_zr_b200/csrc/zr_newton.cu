@@ -58,7 +58,8 @@ constexpr int kEpiWarps = 8;                               // two for each 32 ro
 constexpr int kPartBytes = 32 * 128;                       // a warp's 32 rows of 64 fp16 columns
 constexpr int kBufBytes = 2 * kPartBytes;                  // X and its rounding error; or a result and its mirror image; or 32 x 64 fp32
 constexpr int kDiagBytes = 64 * 4;                         // a warp's 64 columns of a diagonal
-constexpr int kIterThreads = 64 + 32 * kEpiWarps;          // producer, issuer, epilogue warps
+constexpr int kIterThreads = 96 + 32 * kEpiWarps;          // producer of op1, issuer, epilogue warps, producer of op2
+constexpr int kOp2Warp = 2 + kEpiWarps;
 constexpr int kSmemStaging = kStages * kStageBytes, kSmemDiag = kSmemStaging + kEpiWarps * kBufBytes;
 constexpr int kSmemBars = kSmemDiag + kEpiWarps * kDiagBytes;
 constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
@@ -72,7 +73,7 @@ enum : int { kGram = 0, kPoly = 1, kUpdate = 2 };          // products of a step
 // the epilogue's, as in NsMaps.
 struct IterMaps {
     CUtensorMap gram1[2], gram2[2], poly1, poly2, update1[2], update2[2];
-    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;
+    CUtensorMap ex[2], egram, epoly, mgram, mpoly;
 };
 
 struct IterGroup {
@@ -197,8 +198,9 @@ __device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const Tile
 // counter's round trip where it paid a launch.  The walk is in dependency
 // order and the launch cooperative (every pair resident), so each wait ends.
 //
-// Per CTA: warp 0 feeds a ring of five 32 KB stages by TMA (128 rows of op1,
-// half of op2's columns), the leader's warp 1 issues the pair's tensor-core
+// Per CTA: warps 0 and 10 feed a ring of five 32 KB stages by TMA (128 rows of
+// op1, half of op2's columns; a copy takes its lane some 200 cycles to issue,
+// so each has its own), the leader's warp 1 issues the pair's tensor-core
 // instructions into one of two accumulators, warps 2 to 9 empty the other
 // one, so a tile's epilogue runs under the next tile's products.  256 x 256
 // tiles on a pair move 64 bytes per SM and clock at the tensor cores' full
@@ -248,48 +250,51 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == kOp2Warp) {
         if (elect_one()) {
-            fence_async_global();      // the kernel before this one wrote X_0 by ordinary stores
+            const bool first = warp == 0;
             const uint32_t pair_full = leader_address(full);
-            uint32_t it = 0, seen = 0;
+            fence_async_global();      // the kernel before this one wrote X_0 by ordinary stores
+            uint32_t s = 0, phase = 1, seen = 0;
             bool ok = true;
             for (TileWalk<NG> walk(L, pair); ok && walk.live(); walk.next()) {
                 const TileAt at = walk.at();
                 const IterGroup& g = L.g[at.group];
+                const IterMaps& maps = L.maps.of(at.group);
+                const int from = at.step & 1;
+                const CUtensorMap* map =
+                    first ? (at.op == kGram ? &maps.gram1[from] : at.op == kPoly ? &maps.poly1 : &maps.update1[from])
+                          : (at.op == kGram ? &maps.gram2[from] : at.op == kPoly ? &maps.poly2 : &maps.update2[from]);
                 const uint32_t need = shares_before(g, at);
                 if (need != 0) {
                     if (!count_wait(g.done + at.slot, need, bail)) break;
                     fence_async_global();
                 }
-                s_ready = ++seen;
-                const int from = at.step & 1;
-                const IterMaps& maps = L.maps.of(at.group);
-                const bool mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
-                const CUtensorMap* op1 = at.op == kGram ? &maps.gram1[from] : at.op == kPoly ? &maps.poly1 : &maps.update1[from];
-                const CUtensorMap* op2 = at.op == kGram ? &maps.gram2[from] : at.op == kPoly ? &maps.poly2 : &maps.update2[from];
+                if (first) s_ready = ++seen;
                 const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
                 const int32_t nk = (k + kBK - 1) / kBK;
                 // A box of a K-major operand is 64 contraction indices x 64 or
                 // 128 rows; of an MN-major one, one or two chunks of 64 columns
-                // x 64 contraction indices (one chunk: rows as they are).
-                const int32_t r0 = at.row0 + rank * 128, c0 = at.col0 + rank * (at.bn / 2);
-                const bool chunks2 = mn2 && at.bn == kBN;
+                // x 64 contraction indices (one chunk: columns as they are).
+                const bool mn = first ? at.op == kGram && g.tall : at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
+                const bool two = first || at.bn == kBN;
+                const int32_t at0 = first ? at.row0 + rank * 128 : at.col0 + rank * (at.bn / 2);
+                int32_t x = mn && !two ? at0 : 0, y = mn ? 0 : at0;
+                const int32_t z = mn && two ? at0 / 64 : 0, dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
                 const uint32_t bytes = 2 * (kOpBytes + at.bn / 128 * kBoxBytes);
-                for (int32_t kb = 0; kb < nk; ++kb, ++it) {
-                    const uint32_t s = it % kStages, phase = (it / kStages) & 1;
-                    if (!mbar_wait(empty + 8 * s, phase ^ 1, bail)) {
+                for (int32_t kb = 0; kb < nk; ++kb, x += dx, y += dy) {
+                    if (!mbar_wait(empty + 8 * s, phase, bail)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = smem + s * kStageBytes;
-                    if (rank == 0) mbar_expect(full + 8 * s, bytes);
-                    const uint32_t bar = pair_full + 8 * s;
-                    const int k0 = kb * kBK;
-                    if (mn1) tma_load_chunks(dst, op1, k0, r0 / 64, at.slot, bar);
-                    else tma_load_pair(dst, op1, k0, r0, at.slot, bar);
-                    if (chunks2) tma_load_chunks(dst + kOpBytes, op2, k0, c0 / 64, at.slot, bar);
-                    else tma_load_pair(dst + kOpBytes, op2, mn2 ? c0 : k0, mn2 ? k0 : c0, at.slot, bar);
+                    // (op2's bytes may arrive before op1's lane announces them:
+                    // the phase still waits for that lane)
+                    if (first && rank == 0) mbar_expect(full + 8 * s, bytes);
+                    tma_load_pair(smem + s * kStageBytes + (first ? 0 : kOpBytes), map, x, y, z, at.slot, pair_full + 8 * s);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }
@@ -347,13 +352,11 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             const int32_t chunks = row_w < rows ? (min(at.bn, cols - at.col0) + 63) / 64 : 0;
             const uint32_t buf = acc & 1;
             const IterMaps& maps = L.maps.of(at.group);
-            const CUtensorMap* in_hi = at.op == kPoly ? &maps.egram : &maps.exh[at.step & 1];
-            const CUtensorMap* in_lo = &maps.exl[at.step & 1];
             auto load = [&](int ch) {              // lane 0: the elementwise operand of a chunk
                 const int32_t x = at.col0 + ch * 64;
                 mbar_expect(in_bar, sym ? kPartBytes : 2 * kPartBytes);
-                tma_load(hi, in_hi, x, row_w, at.slot, in_bar);
-                if (!sym) tma_load(lo, in_lo, x, row_w, at.slot, in_bar);
+                if (sym) tma_load_3d(hi, &maps.egram, x, row_w, at.slot, in_bar);
+                else tma_load_4d(hi, &maps.ex[at.step & 1], x, row_w, 0, at.slot, in_bar);
             };
             const Affine k = L.k[last ? 3 : at.op];
             const float* diag = (at.op == kPoly ? g.gram_diag : g.poly_diag) + static_cast<int64_t>(at.slot) * g.dim;
@@ -514,12 +517,11 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     __syncwarp();
                     if (one) {
                         if (sym) {
-                            tma_store(at.op == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
+                            tma_store_3d(at.op == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
                             if (mirror)
-                                tma_store(at.op == kGram ? &maps.mgram : &maps.mpoly, row_w, c, at.slot, lo);
+                                tma_store_3d(at.op == kGram ? &maps.mgram : &maps.mpoly, row_w, c, at.slot, lo);
                         } else {
-                            tma_store(&maps.exh[(at.step & 1) ^ 1], c, row_w, at.slot, hi);
-                            tma_store(&maps.exl[(at.step & 1) ^ 1], c, row_w, at.slot, lo);
+                            tma_store_4d(&maps.ex[(at.step & 1) ^ 1], c, row_w, 0, at.slot, hi);
                         }
                         store_commit();
                         if (at.op != kGram && ch + 2 < chunks) {
@@ -846,36 +848,28 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A batch of rows x cols fp16 matrices with rows of ld elements, copied in
-// boxes of box_cols x box_rows; what lies outside a matrix reads as zero and
-// is not written.
-int encode_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld, int box_cols = 64,
-               int box_rows = 64, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+// Copies of a batch of cols x rows fp16 matrices, or of `parts` such batches
+// part_bytes apart: boxes of box_cols x box_rows x box_parts.  What lies
+// outside a matrix reads as zero and is not written.
+int encode_map(CUtensorMap* map, int dimensions, void* base, int64_t cols, int64_t rows, int64_t parts, int64_t batch,
+               int64_t row_bytes, int64_t part_bytes, int64_t matrix_bytes, int box_cols, int box_rows, int box_parts,
+               CUtensorMapSwizzle swizzle) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t unit[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
-// The same matrices as chunks of 64 columns, copied two at a time, 64 rows
-// each.  The last chunk reaches into the rows' padding: its columns are rows
-// or columns of a product that no result keeps.
-int encode_chunks(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld) {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>((cols + 63) / 64),
-                                static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(ld) * rows * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1}, unit[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts),
+                          static_cast<cuuint64_t>(batch)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(part_bytes),
+                             static_cast<cuuint64_t>(matrix_bytes)};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
+                         static_cast<cuuint32_t>(box_parts), 1};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    if (dimensions == 3) {
+        dims[2] = dims[3];
+        strides[1] = strides[2];
+        box[2] = 1;
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dimensions, base, dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
@@ -964,8 +958,7 @@ void fill_maps(IterMaps& o, const NsGroup& s, Tiling t) {
         o.gram2[j] = sym_half ? m.x_box[j] : o.gram1[j];
         o.update1[j] = tall ? m.x_rows[j] : m.poly_rows;
         o.update2[j] = tall ? (out_half ? m.poly_box : m.poly_rows) : out_half ? m.x_box[j] : m.x_chunks[j];
-        o.exh[j] = m.exh[j];
-        o.exl[j] = m.exl[j];
+        o.ex[j] = m.ex[j];
     }
     o.poly1 = m.gram_rows;
     o.poly2 = sym_half ? m.gram_box : m.gram_rows;
@@ -1121,27 +1114,36 @@ int ns_bind_scratch(NsGroup& g, void* base) {
     g.done = reinterpret_cast<uint32_t*>(p + 4 * x + 2 * a + 2 * d);
     NsMaps& t = g.maps;
     int e = cudaSuccess;
-    auto encode = [&](CUtensorMap* map, void* at, bool gram, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
-        if (e != cudaSuccess) return;
-        e = gram ? encode_map(map, at, g.gram_dim(), g.gram_dim(), g.batch, g.ldg(), box_cols, box_rows, swizzle)
-                 : encode_map(map, at, g.n, g.m, g.batch, g.ld(), box_cols, box_rows, swizzle);
-    };
+    const int64_t dim = g.gram_dim(), x_row = 2 * g.ld(), a_row = 2 * g.ldg();
     constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, kNone = CU_TENSOR_MAP_SWIZZLE_NONE;
+    auto box = [&](CUtensorMap* map, void* at, bool gram, int rows) {          // an operand's: 64 x rows
+        if (e != cudaSuccess) return;
+        e = gram ? encode_map(map, 4, at, dim, dim, 1, g.batch, a_row, dim * a_row, dim * a_row, 64, rows, 1, k128)
+                 : encode_map(map, 4, at, g.n, g.m, 1, g.batch, x_row, g.m * x_row, g.m * x_row, 64, rows, 1, k128);
+    };
+    auto share = [&](CUtensorMap* map, void* at, int cols, int rows, CUtensorMapSwizzle swizzle) {
+        if (e == cudaSuccess)
+            e = encode_map(map, 3, at, dim, dim, 1, g.batch, a_row, 0, dim * a_row, cols, rows, 1, swizzle);
+    };
     for (int i = 0; i < 2; ++i) {
-        encode(&t.x_box[i], g.xh[i], false, 64, 64, k128);
-        encode(&t.x_rows[i], g.xh[i], false, 64, 128, k128);
-        if (e == cudaSuccess) e = encode_chunks(&t.x_chunks[i], g.xh[i], g.n, g.m, g.batch, g.ld());
-        encode(&t.exh[i], g.xh[i], false, 64, 32, k128);
-        encode(&t.exl[i], g.xl[i], false, 64, 32, k128);
+        box(&t.x_box[i], g.xh[i], false, 64);
+        box(&t.x_rows[i], g.xh[i], false, 128);
+        // chunks of 64 columns, two at a time: the last reaches into the rows'
+        // padding, whose columns are rows or columns of a product that no
+        // result keeps
+        if (e == cudaSuccess)
+            e = encode_map(&t.x_chunks[i], 4, g.xh[i], 64, g.m, (g.n + 63) / 64, g.batch, x_row, 128, g.m * x_row, 64, 64, 2, k128);
+        if (e == cudaSuccess)
+            e = encode_map(&t.ex[i], 4, g.xh[i], g.n, g.m, 2, g.batch, x_row, static_cast<int64_t>(x), g.m * x_row, 64, 32, 2, k128);
     }
-    encode(&t.gram_box, g.gram, true, 64, 64, k128);
-    encode(&t.gram_rows, g.gram, true, 64, 128, k128);
-    encode(&t.poly_box, g.poly, true, 64, 64, k128);
-    encode(&t.poly_rows, g.poly, true, 64, 128, k128);
-    encode(&t.egram, g.gram, true, 64, 32, k128);
-    encode(&t.epoly, g.poly, true, 64, 32, k128);
-    encode(&t.mgram, g.gram, true, 32, 64, kNone);
-    encode(&t.mpoly, g.poly, true, 32, 64, kNone);
+    box(&t.gram_box, g.gram, true, 64);
+    box(&t.gram_rows, g.gram, true, 128);
+    box(&t.poly_box, g.poly, true, 64);
+    box(&t.poly_rows, g.poly, true, 128);
+    share(&t.egram, g.gram, 64, 32, k128);
+    share(&t.epoly, g.poly, 64, 32, k128);
+    share(&t.mgram, g.gram, 32, 64, kNone);
+    share(&t.mpoly, g.poly, 32, 64, kNone);
     return e;
 }
 

@@ -11,11 +11,11 @@ namespace zr {
 
 // Tensor maps of a group's scratch.  The products' operands: boxes of 64
 // columns x 64 or 128 rows, and two chunks of 64 columns x 64 rows.  An
-// epilogue warp's share of X, its rounding error, A and B: 64 columns x 32
-// rows, and the transposed shares of A and B.
+// epilogue warp's share of X with its rounding error, of A and of B: 64
+// columns x 32 rows, and the transposed shares of A and B.
 struct NsMaps {
     CUtensorMap x_box[2], x_rows[2], x_chunks[2], gram_box, gram_rows, poly_box, poly_rows;
-    CUtensorMap exh[2], exl[2], egram, epoly, mgram, mpoly;
+    CUtensorMap ex[2], egram, epoly, mgram, mpoly;
 };
 
 // Matrices of one shape: source, scratch and destination.  Gram matrices
