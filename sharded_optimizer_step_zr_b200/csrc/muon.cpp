@@ -265,8 +265,7 @@ zr_status zr_orthogonalize(const void* x, int32_t dtype, int64_t batch, int64_t 
                                               stream));
     if (zr::ns_bind_scratch(g, base + need - zr::ns_scratch_bytes(batch, m, n)) != cudaSuccess) return ZR_ERR_CUDA;
     int e = zr::launch_ns_sumsq(g, gave_up, stream);
-    if (e == cudaSuccess) e = zr::launch_ns_scales(&g, 1, ns->eps, stream);
-    if (e == cudaSuccess) e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, zr::NsApply(), nullptr, gave_up, stream);
+    if (e == cudaSuccess) e = zr::launch_ns_iterations(&g, 1, ns->steps, coeffs, ns->eps, zr::NsApply(), nullptr, gave_up, stream);
     return cuda_status(e);
 }
 
@@ -345,6 +344,7 @@ zr_status zr_muon_set_workspace(zr_muon* u, void* d_ws, uint64_t bytes, zr_strea
         g.src_dtype = ZR_DTYPE_F32;
         g.src_row = g.n;
         g.src_batch = zr::ns_source_pitch(g.m, g.n);
+        g.n_partials = static_cast<int32_t>((g.m * g.n + zr::kMuonTileElems - 1) / zr::kMuonTileElems);
         g.scale = reinterpret_cast<float2*>(base + u->at_scale) + first;
         g.partials = reinterpret_cast<double*>(base + u->at_partials);
         g.first_partial = reinterpret_cast<const int32_t*>(base + u->at_first) + first;
@@ -419,9 +419,7 @@ zr_status zr_muon_step(const zr_muon* u, const void* const* grad_ptrs, float* ma
     if (zr::ns_small(groups.data(), n, true))
         return cuda_status(zr::launch_ns_small(groups.data(), n, u->hp.ns.steps, coeffs, u->hp.ns.eps, apply, gave_up,
                                               false, stream));
-    e = zr::launch_ns_scales(groups.data(), n, u->hp.ns.eps, stream);
-    if (e == cudaSuccess)
-        e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, apply, u->d_workspace + u->at_maps, gave_up,
+    e = zr::launch_ns_iterations(groups.data(), n, u->hp.ns.steps, coeffs, u->hp.ns.eps, apply, u->d_workspace + u->at_maps, gave_up,
                                      stream);
     return cuda_status(e);
 }

@@ -58,8 +58,7 @@ constexpr int kEpiWarps = 8;                               // two for each 32 ro
 constexpr int kPartBytes = 32 * 128;                       // a warp's 32 rows of 64 fp16 columns
 constexpr int kBufBytes = 2 * kPartBytes;                  // X and its rounding error; or a result and its mirror image; or 32 x 64 fp32
 constexpr int kDiagBytes = 64 * 4;                         // a warp's 64 columns of a diagonal
-constexpr int kIterThreads = 96 + 32 * kEpiWarps;          // producer of op1, issuer, epilogue warps, producer of op2
-constexpr int kOp2Warp = 2 + kEpiWarps;
+constexpr int kIterThreads = 64 + 32 * kEpiWarps;          // producer, issuer, epilogue warps
 constexpr int kSmemStaging = kStages * kStageBytes, kSmemDiag = kSmemStaging + kEpiWarps * kBufBytes;
 constexpr int kSmemBars = kSmemDiag + kEpiWarps * kDiagBytes;
 constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
@@ -198,9 +197,8 @@ __device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const Tile
 // counter's round trip where it paid a launch.  The walk is in dependency
 // order and the launch cooperative (every pair resident), so each wait ends.
 //
-// Per CTA: warps 0 and 10 feed a ring of five 32 KB stages by TMA (128 rows of
-// op1, half of op2's columns; a copy takes its lane some 200 cycles to issue,
-// so each has its own), the leader's warp 1 issues the pair's tensor-core
+// Per CTA: warp 0 feeds a ring of five 32 KB stages by TMA (128 rows of op1,
+// half of op2's columns, one copy each), the leader's warp 1 issues the pair's tensor-core
 // instructions into one of two accumulators, warps 2 to 9 empty the other
 // one, so a tile's epilogue runs under the next tile's products.  256 x 256
 // tiles on a pair move 64 bytes per SM and clock at the tensor cores' full
@@ -250,9 +248,8 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
 
-    if (warp == 0 || warp == kOp2Warp) {
+    if (warp == 0) {
         if (elect_one()) {
-            const bool first = warp == 0;
             const uint32_t pair_full = leader_address(full);
             fence_async_global();      // the kernel before this one wrote X_0 by ordinary stores
             uint32_t s = 0, phase = 1, seen = 0;
@@ -262,35 +259,33 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 const IterGroup& g = L.g[at.group];
                 const IterMaps& maps = L.maps.of(at.group);
                 const int from = at.step & 1;
-                const CUtensorMap* map =
-                    first ? (at.op == kGram ? &maps.gram1[from] : at.op == kPoly ? &maps.poly1 : &maps.update1[from])
-                          : (at.op == kGram ? &maps.gram2[from] : at.op == kPoly ? &maps.poly2 : &maps.update2[from]);
+                const CUtensorMap* op1 = at.op == kGram ? &maps.gram1[from] : at.op == kPoly ? &maps.poly1 : &maps.update1[from];
+                const CUtensorMap* op2 = at.op == kGram ? &maps.gram2[from] : at.op == kPoly ? &maps.poly2 : &maps.update2[from];
                 const uint32_t need = shares_before(g, at);
                 if (need != 0) {
                     if (!count_wait(g.done + at.slot, need, bail)) break;
                     fence_async_global();
                 }
-                if (first) s_ready = ++seen;
+                s_ready = ++seen;
                 const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
                 const int32_t nk = (k + kBK - 1) / kBK;
                 // A box of a K-major operand is 64 contraction indices x 64 or
                 // 128 rows; of an MN-major one, one or two chunks of 64 columns
                 // x 64 contraction indices (one chunk: columns as they are).
-                const bool mn = first ? at.op == kGram && g.tall : at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
-                const bool two = first || at.bn == kBN;
-                const int32_t at0 = first ? at.row0 + rank * 128 : at.col0 + rank * (at.bn / 2);
-                int32_t x = mn && !two ? at0 : 0, y = mn ? 0 : at0;
-                const int32_t z = mn && two ? at0 / 64 : 0, dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
+                const bool mn1 = at.op == kGram && g.tall, mn2 = at.op == kGram ? g.tall : at.op == kUpdate && !g.tall;
+                const bool chunks2 = mn2 && at.bn == kBN;
+                const int32_t r0 = at.row0 + rank * 128, c0 = at.col0 + rank * (at.bn / 2);
                 const uint32_t bytes = 2 * (kOpBytes + at.bn / 128 * kBoxBytes);
-                for (int32_t kb = 0; kb < nk; ++kb, x += dx, y += dy) {
+                for (int32_t kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(empty + 8 * s, phase, bail)) {
                         ok = false;
                         break;
                     }
-                    // (op2's bytes may arrive before op1's lane announces them:
-                    // the phase still waits for that lane)
-                    if (first && rank == 0) mbar_expect(full + 8 * s, bytes);
-                    tma_load_pair(smem + s * kStageBytes + (first ? 0 : kOpBytes), map, x, y, z, at.slot, pair_full + 8 * s);
+                    const int32_t k0 = kb * kBK;
+                    const uint32_t dst = smem + s * kStageBytes, bar = pair_full + 8 * s;
+                    if (rank == 0) mbar_expect(full + 8 * s, bytes);
+                    tma_load_pair(dst, op1, mn1 ? 0 : k0, mn1 ? k0 : r0, mn1 ? r0 / 64 : 0, at.slot, bar);
+                    tma_load_pair(dst + kOpBytes, op2, !mn2 ? k0 : chunks2 ? 0 : c0, mn2 ? k0 : c0, chunks2 ? c0 / 64 : 0, at.slot, bar);
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1;
@@ -692,7 +687,7 @@ struct PrepGroup {
 struct PrepLaunch {
     int32_t n_groups;
     uint32_t *abort_word, *gave_up;
-    int32_t total_matrices;
+    int32_t total_matrices, own_scale;    // own_scale: every CTA of the start kernel adds up its matrix's partials
     double eps;
     PrepGroup g[kMaxGroups];
 };
@@ -780,19 +775,25 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_sumsq_kernel(const __grid_
     if (threadIdx.x == 0) g.partials[static_cast<int64_t>(at.slot) * g.n_partials + at.piece] = sum;
 }
 
-// One CTA per matrix: the norm.
+// A matrix's scale from its partials, in a fixed order; valid in thread 0.
+__device__ __forceinline__ float2 matrix_scale(const PrepGroup& g, int32_t slot, double eps) {
+    const int64_t first = g.first_partial ? g.first_partial[slot] : static_cast<int64_t>(slot) * g.n_partials;
+    const int64_t last = g.first_partial ? g.first_partial[slot + 1] : first + g.n_partials;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int64_t i = first + threadIdx.x; i < last; i += kPrepThreads) sum += __ldcg(g.partials + i);
+    return ns_scale_of(prep_block_sum(sum), eps);
+}
+
+// One CTA per matrix, for matrices of many partials.
 __global__ void __launch_bounds__(kPrepThreads) zr_ns_scale_kernel(const __grid_constant__ PrepLaunch L) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     int32_t slot = blockIdx.x, gi = 0;
     while (slot >= L.g[gi].batch) slot -= L.g[gi++].batch;
     const PrepGroup& g = L.g[gi];
-    const int64_t first = g.first_partial ? g.first_partial[slot] : static_cast<int64_t>(slot) * g.n_partials;
-    const int64_t last = g.first_partial ? g.first_partial[slot + 1] : first + g.n_partials;
-    double sum = 0.0;
-    for (int64_t i = first + threadIdx.x; i < last; i += kPrepThreads) sum += __ldcg(g.partials + i);
-    sum = prep_block_sum(sum);
-    if (threadIdx.x == 0) g.scale[slot] = ns_scale_of(sum, L.eps);
+    const float2 scale = matrix_scale(g, slot, L.eps);
+    if (threadIdx.x == 0) g.scale[slot] = scale;
 }
 
 __global__ void __launch_bounds__(kPrepThreads) zr_ns_start_kernel(const __grid_constant__ PrepLaunch L) {
@@ -804,8 +805,17 @@ __global__ void __launch_bounds__(kPrepThreads) zr_ns_start_kernel(const __grid_
         g.done[at.slot] = 0u;
         if (at.group == 0 && at.slot == 0) *L.abort_word = 0u;
     }
+    float2 s;
+    if (L.own_scale) {
+        __shared__ float2 own;
+        const float2 mine = matrix_scale(g, at.slot, L.eps);
+        if (threadIdx.x == 0) own = mine;
+        __syncthreads();
+        s = own;
+    } else {
+        s = g.scale[at.slot];
+    }
     if (at.col >= g.cols) return;
-    const float2 s = g.scale[at.slot];
     const int64_t out = (static_cast<int64_t>(at.slot) * g.rows + at.row0) * g.ld + at.col;
 #pragma unroll
     for (int r = 0; r < kPrepRows; ++r) {
@@ -928,12 +938,12 @@ int resident_pairs() {
 }
 
 // 256-column tiles, or 128 where that gives the pairs an evener share.  In
-// cycles: 64 contraction indices take a pair 620 or 413 (each SM takes in
-// some 55 bytes per clock), what follows a wave's products some 7000 or 5000.
+// cycles: 64 contraction indices take a pair 520 or 400, what follows a wave's
+// products some 9000 or 4000.
 int pick_columns(int64_t tiles256, int64_t tiles128, int64_t pairs, int64_t k) {
     const int64_t waves256 = (tiles256 + pairs - 1) / pairs, waves128 = (tiles128 + pairs - 1) / pairs;
     const int64_t blocks = (k + kBK - 1) / kBK;
-    return waves128 * blocks * 413 + 5000 < waves256 * blocks * 620 + 7000 ? 128 : 256;
+    return waves128 * blocks * 400 + 4000 < waves256 * blocks * 520 + 9000 ? 128 : 256;
 }
 
 struct Tiling { int sym_bn, out_bn; };
@@ -1156,19 +1166,7 @@ int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream) {
     return d.run(zr_ns_sumsq_kernel, L);
 }
 
-int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* stream) {
-    for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
-        PrepLaunch L{};
-        fill_prep(L, groups + at, std::min(kMaxGroups, n_groups - at));
-        L.eps = eps;
-        Dependent<PrepLaunch> d(static_cast<unsigned>(L.total_matrices), kPrepThreads, 0, stream);
-        const cudaError_t e = d.run(zr_ns_scale_kernel, L);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
-int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
+int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
                          const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream) {
     const IterMaps* maps = static_cast<const IterMaps*>(device_maps);
     for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
@@ -1177,6 +1175,16 @@ int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps,
         PrepLaunch P{};
         const int64_t pieces = fill_prep(P, gs, n);
         if (pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        P.eps = eps;
+        // Up to 4 partials a thread cost less than a launch.
+        int64_t partials = 0;
+        for (int32_t i = 0; i < n; ++i) partials = std::max<int64_t>(partials, gs[i].n_partials);
+        P.own_scale = partials <= 4 * kPrepThreads;
+        if (!P.own_scale) {
+            Dependent<PrepLaunch> d(static_cast<unsigned>(P.total_matrices), kPrepThreads, 0, stream);
+            const cudaError_t e = d.run(zr_ns_scale_kernel, P);
+            if (e != cudaSuccess) return e;
+        }
         Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
         int e = d.run(zr_ns_start_kernel, P);
         if (e != cudaSuccess) return e;

@@ -80,11 +80,9 @@ int64_t ns_partials_per_matrix(int64_t m, int64_t n);
 // Sums of squares of every source matrix into partials (one CTA per piece),
 // and *gave_up cleared.
 int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream);
-// The matrices' scales 1 / (norm + eps) from the partials.
-int launch_ns_scales(const NsGroup* groups, int32_t n_groups, double eps, void* stream);
-// X_0, then `steps` iterations, then the destination.  *gave_up (device) is
+// The scales 1 / (norm + eps) from the partials, X_0, then `steps` iterations, then the destination.  *gave_up (device) is
 // set to 1 if a wait inside a kernel ran out.
-int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3],
+int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
                          const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream);
 // What several groups' launches need in device memory (device_maps; 128-byte
 // aligned), filled on the host for the current device; a single group needs none.

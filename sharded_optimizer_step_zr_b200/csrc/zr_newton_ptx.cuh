@@ -99,11 +99,6 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
 __device__ __forceinline__ void red_release(uint32_t* p, uint32_t v) {
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -145,9 +140,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const B
     return wait_slow([=] { return mbar_try(bar, parity); }, b);
 }
 __device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t need, const Bail& b) {
-    // polled without ordering, which each acquire would pay for
     if (ld_acquire(p) >= need) return true;
-    return wait_slow([=] { return ld_relaxed(p) >= need; }, b) && ld_acquire(p) >= need;
+    return wait_slow([=] { return ld_acquire(p) >= need; }, b);
 }
 
 // An operand box; its bytes count on the leader's barrier.
