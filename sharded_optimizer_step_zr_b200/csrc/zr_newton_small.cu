@@ -44,6 +44,7 @@ constexpr int kSmallGroups = 16;
 struct SmallGroup {
     const void* src;
     int32_t dtype, tall, g, l, width;           // width: columns of Z on a CTA, a multiple of 64
+    int32_t vec_in, vec_out;                    // four elements of a row move as one word
     int64_t src_row, src_batch;
     int32_t first, n;                           // the group's first cluster; columns of X
     uint16_t* out;
@@ -234,16 +235,47 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
 #pragma unroll 1
         for (int pass = 0; pass * 128 < width; ++pass) {
             // warp w reads rows w, w + 8, ..: 32 lanes along a row
-            const int32_t c0 = col0 + pass * 128 + lane;
-            const int64_t e0 = src0 + warp * g.src_row + c0;
-            float v[64];
-            load_source(
-                g.src, g.dtype, v, [&](int k) { return e0 + 8 * (k >> 2) * g.src_row + 32 * (k & 3); },
-                [&](int k) { return warp + 8 * (k >> 2) < g.g && c0 + 32 * (k & 3) < g.l; });
+            if (g.vec_in) {
+                const int32_t c0 = col0 + pass * 128 + 4 * lane;
+                const int64_t e0 = src0 + warp * g.src_row + c0;
+                uint4 q[16];
+                if (g.dtype == ZR_DTYPE_F32) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-                const int cl = 32 * (k & 3) + lane;
-                st_shared_f32(ex_piece(ex, warp + 8 * (k >> 2), cl >> 2) + 4 * (cl & 3), v[k]);
+                    for (int i = 0; i < 16; ++i)
+                        q[i] = warp + 8 * i < g.g && c0 < g.l
+                                   ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(g.src) + e0 + 8 * i * g.src_row))
+                                   : make_uint4(0, 0, 0, 0);
+                } else {
+                    uint2 u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        u[i] = warp + 8 * i < g.g && c0 < g.l
+                                   ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.src) + e0 + 8 * i * g.src_row))
+                                   : make_uint2(0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (g.dtype == ZR_DTYPE_BF16) {
+                            q[i] = make_uint4(u[i].x << 16, u[i].x & 0xFFFF0000u, u[i].y << 16, u[i].y & 0xFFFF0000u);
+                        } else {
+                            const float2 f = half2_values(u[i].x), h = half2_values(u[i].y);
+                            q[i] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(h.x), __float_as_uint(h.y));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st_shared16(ex_piece(ex, warp + 8 * i, lane), q[i]);
+            } else {
+                const int32_t c0 = col0 + pass * 128 + lane;
+                const int64_t e0 = src0 + warp * g.src_row + c0;
+                float v[64];
+                load_source(
+                    g.src, g.dtype, v, [&](int k) { return e0 + 8 * (k >> 2) * g.src_row + 32 * (k & 3); },
+                    [&](int k) { return warp + 8 * (k >> 2) < g.g && c0 + 32 * (k & 3) < g.l; });
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    const int cl = 32 * (k & 3) + lane;
+                    st_shared_f32(ex_piece(ex, warp + 8 * (k >> 2), cl >> 2) + 4 * (cl & 3), v[k]);
+                }
             }
             __syncthreads();
             if (half == pass) {
@@ -516,6 +548,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
             __syncthreads();
             // 32 lanes along a row; columns past the width are the next CTA's
             const int32_t cols = min(min(width - pass * 128, 128), g.l - (col0 + pass * 128));
+            if (!APPLY && g.vec_out) {
+                uint16_t* out = g.out + slot * g.out_batch + warp * g.out_row + col0 + pass * 128 + 4 * lane;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (warp + 8 * i >= g.g || 4 * lane >= cols) continue;
+                    const uint4 q = ld_shared16(ex_piece(ex, warp + 8 * i, lane));
+                    const uint32_t w0 = bf16_bits(__uint_as_float(q.x)) | (static_cast<uint32_t>(bf16_bits(__uint_as_float(q.y))) << 16);
+                    const uint32_t w1 = bf16_bits(__uint_as_float(q.z)) | (static_cast<uint32_t>(bf16_bits(__uint_as_float(q.w))) << 16);
+                    *reinterpret_cast<uint2*>(out + 8 * i * g.out_row) = make_uint2(w0, w1);
+                }
+                continue;
+            }
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int r0 = warp + 64 * i;
@@ -601,6 +645,11 @@ int launch_small(const NsGroup* groups, int32_t n, int ctas, int32_t steps, cons
         g.width = static_cast<int32_t>((g.l + 64 * ctas - 1) / (64 * ctas) * 64);
         g.src_row = s.src_row;
         g.src_batch = s.src_batch;
+        auto aligned = [&](const void* p, uint64_t bytes, int64_t row, int64_t batch) {
+            return s.n % 4 == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0 && row % 4 == 0 && batch % 4 == 0;
+        };
+        g.vec_in = aligned(s.src, s.src_dtype == ZR_DTYPE_F32 ? 16 : 8, s.src_row, s.src_batch);
+        g.vec_out = s.out != nullptr && aligned(s.out, 8, s.out_row, s.out_batch);
         g.first = static_cast<int32_t>(matrices);
         g.n = static_cast<int32_t>(s.n);
         g.out = s.out;
