@@ -6,15 +6,12 @@ clusters of 1 to 16 CTAs), and the persistent kernel for all others.
 Tolerances as in test_gpu_muon.py: half a bf16 step of the result, and half an
 fp16 step of each iterate.
 """
-import math
-
 import pytest
 import torch
 
 import sharded_optimizer_step_zr_b200 as zr
-from sharded_optimizer_step_zr_b200.muon import ZrMuon, orthogonalize
-from sharded_optimizer_step_zr_b200.plan import ZrPlan
-from test_gpu_muon import DEV, Job, SETS, assert_orthogonal, quantize, randn, read_back
+from sharded_optimizer_step_zr_b200.muon import orthogonalize
+from test_gpu_muon import DEV, Job, assert_orthogonal, quantize, randn, read_back
 
 pytestmark = pytest.mark.gpu
 
@@ -166,8 +163,8 @@ def test_more_shapes_than_a_launch_holds(least):
 
 @pytest.mark.parametrize("name", ["small", "large"])
 def test_gather_targets_on_each_path(name):
-    job = Job(PATHS[name], 2, 1, seed=5, layout=zr.ZR_PARAMS_GLOBAL)
-    targets = [torch.full_like(job.param, 3.0) for _ in range(3)]
+    job = Job(PATHS[name], 3, 1, seed=5, layout=zr.ZR_PARAMS_GLOBAL)
+    targets = [torch.full_like(job.param, 3.0) for _ in range(3)]          # one per rank
     zr.zr_plan_set_gather_targets(job.plan.handle, targets)
     job.new_grads()
     job.muon.step(job.grads, job.master, job.momentum, None)
