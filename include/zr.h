@@ -613,7 +613,10 @@ typedef struct {
  * out need their element's alignment only.  batch, m or n of 0: nothing to
  * do, ZR_OK.
  * The workspace (zr_orthogonalize_workspace_bytes, 256-byte aligned) holds
- * fp16 copies; calls that share one must be ordered on the GPU.  Its first
+ * fp16 copies; calls that share one must be ordered on the GPU.  Matrices
+ * whose smaller extent is above 128 (or the larger above 4096) run in a
+ * cooperative kernel on up to every SM: it starts once they are free, and
+ * calls on several streams follow one another.  The workspace's first
  * 32-bit word is 0 after a completed call; 1 says that a wait inside a
  * kernel ran out and the results are not valid (not expected; the
  * alternative would be a hang).

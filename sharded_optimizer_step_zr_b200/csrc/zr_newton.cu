@@ -7,8 +7,11 @@
 // operand is ever transposed in memory).  A pass over the m x n matrix costs
 // g^2 l multiply-adds for A, g^3 for A A (g = min, l = max) and g^2 l for
 // B X; A and A A are symmetric and only the tiles that touch the lower
-// triangle are computed, each stored twice.  This is bound by the tensor
-// cores for every matrix of a model; the small ones are bound by launches.
+// triangle are computed, each stored twice.  Large matrices are bound by the
+// tensor cores (and they by the power limit), small ones by the way from one
+// product to the next: one persistent kernel runs all of them.  Matrices with
+// a smaller extent of at most 128 have a kernel of their own
+// (zr_newton_small.cu).
 //
 // Number formats.  Operands are fp16, not bf16: the same tensor-core rate,
 // and three more bits -- the rounding of X, A and B is what the result's
@@ -198,16 +201,27 @@ __device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const Tile
 // order and the launch cooperative (every pair resident), so each wait ends.
 //
 // Per CTA: warp 0 feeds a ring of five 32 KB stages by TMA (128 rows of op1,
-// half of op2's columns, one copy each), the leader's warp 1 issues the pair's tensor-core
-// instructions into one of two accumulators, warps 2 to 9 empty the other
-// one, so a tile's epilogue runs under the next tile's products.  256 x 256
-// tiles on a pair move 64 bytes per SM and clock at the tensor cores' full
-// rate, where 128 x 256 on one SM moved 96, which L2 does not sustain.
+// half of op2's columns, one copy each), the leader's warp 1 issues the
+// pair's tensor-core instructions into one of two accumulators, warps 2 to 9
+// empty the other one, so a tile's epilogue runs under the next tile's
+// products.  An SM takes in 64 bytes per clock at most.  256 x 256 tiles on a
+// pair need just that at the tensor cores' full rate (measured: 512 cycles
+// per 64 contraction indices, the ideal, in A; 500 in A A; 570 to 620 in the
+// update, whose epilogue reads and writes twice as much); 256 x 128 tiles
+// need 96 and take 400 cycles in place of 256, but spread few tiles over more
+// SMs; 128 x 256 on one SM would need 96 too.
 //
 // Two epilogue warps share 32 rows.  A warp's elementwise operand comes by
 // TMA into its staging buffer of 32 x 64 and the result leaves from there by
-// TMA, both halves of a row in place; a symmetric result below the diagonal blocks is
-// staged a second time transposed.
+// TMA, both halves of a row in place; a symmetric result below the diagonal
+// blocks is staged a second time transposed.
+//
+// Measured (five steps, a pass among others): 3 x 2048 x 8192 1.82 ms = 920
+// TFLOP/s of useful work and 11008 x 4096 2.93 ms = 1060, at 1.2 to 1.3 GHz
+// under the power limit (79 % of the tensor pipe's cycles; a library's fp16
+// product of the same operands sustains 1250 to 1310); 512 x 512 99 us, 15
+// products of some 11 k cycles: 3 k of copies and products, 4 k to the
+// result's visibility, 2 k to the next product's first load.
 template <int NG, bool APPLY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIterThreads, 1)
 zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {

@@ -12,8 +12,12 @@
 //          128 / C rows in the order of the CTAs),
 //   B    = b A + c A A                        (each CTA for itself),
 //   Z_c <- (a + D) Z_c + R Z_c                (local).
-// 128 x 128: 91 us for five steps in the persistent kernel, TIME_128 us here;
-// 100 x 2000: BEFORE_2000 and TIME_2000.
+// Five steps of 128 x 128: 81 us in the persistent kernel, 27 here; 100 x
+// 2000: 104 and 51; 24 of 128 x 4096: 392 and 244; 150 of 128 x 128: 153 and
+// 51.  So it is taken wherever it fits.  A step of 128 x 256 is 7.4 k cycles:
+// 3.5 k of products with the way into and out of tensor memory, the rest is
+// the epilogues' arithmetic; with C > 1 the exchange adds 5 to 8 k, bound by
+// the distributed shared memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -103,20 +107,19 @@ __device__ __forceinline__ void st_cluster8(uint32_t addr, uint32_t x, uint32_t 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
-// N elements at src + i0 + k * step, of which those with ok(k) exist; zeros
-// elsewhere.  All loads are issued before the first is used.
+// N elements, number k at src[at(k)] if ok(k), else zero.  All loads are issued before the first is used.
 template <int N, typename At, typename Ok>
 __device__ __forceinline__ void load_source(const void* src, int32_t dtype, float (&v)[N], At at, Ok ok) {
     if (dtype == ZR_DTYPE_F32) {
         const float* p = static_cast<const float*>(src);
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = ok(k) ? __ldg(p + at(k)) : 0.0f;
+        for (int k = 0; k < N; ++k) v[k] = ok(k) ? p[at(k)] : 0.0f;
         return;
     }
     const uint16_t* p = static_cast<const uint16_t*>(src);
     uint16_t u[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) u[k] = ok(k) ? __ldg(p + at(k)) : static_cast<uint16_t>(0);
+    for (int k = 0; k < N; ++k) u[k] = ok(k) ? p[at(k)] : static_cast<uint16_t>(0);
 #pragma unroll
     for (int k = 0; k < N; ++k)
         v[k] = dtype == ZR_DTYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(u[k]) << 16) : half_value(u[k]);
@@ -243,14 +246,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) zr_ns_small_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         q[i] = warp + 8 * i < g.g && c0 < g.l
-                                   ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(g.src) + e0 + 8 * i * g.src_row))
+                                   ? *reinterpret_cast<const uint4*>(static_cast<const float*>(g.src) + e0 + 8 * i * g.src_row)
                                    : make_uint4(0, 0, 0, 0);
                 } else {
                     uint2 u[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         u[i] = warp + 8 * i < g.g && c0 < g.l
-                                   ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.src) + e0 + 8 * i * g.src_row))
+                                   ? *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.src) + e0 + 8 * i * g.src_row)
                                    : make_uint2(0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
