@@ -51,7 +51,7 @@ DEFAULT_CONFIG = "llama_7b_w64"
 # timed in the same run after the headline workload, each with its own roofline, clocks and CPU baseline
 COMPANIONS = ("gpt2_124m_w8", "gpt_1p3b_w8_whole_clip")
 FALLBACK_HBM_GBS = 6650.0
-KERNEL_SOURCE = os.path.join(ROOT, "sharded_optimizer_step_zr_b200", "csrc", "zr_kernels.cu")
+KERNEL_SOURCES = [os.path.join(ROOT, "sharded_optimizer_step_zr_b200", "csrc", f) for f in ("zr_kernels.cu", "zr_fold.cuh")]
 PROFILES = os.path.join(ROOT, "profiles")
 
 
@@ -169,8 +169,11 @@ def measured_peak():
 
 
 def kernel_source_hash():
-    with open(KERNEL_SOURCE, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+    h = hashlib.sha256()
+    for path in KERNEL_SOURCES:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
 
 
 def recorded_traffic(workload_name, clip, owned_params):
