@@ -99,42 +99,60 @@ __global__ void __launch_bounds__(kThreads) zr_muon_kernel(const GradPtrs<CAP> g
     const MuonTile tile = a.tiles[blockIdx.x];
     const int lane = threadIdx.x & 31;
     double sq = 0.0;
-    for (int it = 0; it < kMuonTileElems / (kThreads * 8); ++it) {
-        const int e = (it * kThreads + static_cast<int>(threadIdx.x)) * 8;
-        if ((e & ~(kMuonBlock - 1)) >= tile.len) break;       // the whole warp
-        const int n = max(0, min(8, tile.len - e));
-        const bool vec = n == 8 && tile.aligned;
-        const int64_t o = tile.owned + e;
-        const int64_t block = tile.scale + e / kMuonBlock;
-        float x[8];
-        if constexpr (OP == Op::kQuantize) {
-            load_f32(a.momentum + o, vec, n, x);
-            store_block(a.codes + o, a.scales + block, vec, n, lane, x);
-        } else if constexpr (OP == Op::kDequantize) {
-            load_codes(a.codes + o, vec, n, a.scales[block], x);
-            store_f32(a.momentum + o, vec, n, x);
-        } else {
-            if constexpr (EIGHT_BIT) load_codes(a.codes + o, vec, n, a.scales[block], x);
-            else load_f32(a.momentum + o, vec, n, x);
-            float g[8];
-            if (vec) {
-                fold8<CAP, G>(gp, a.world_size, o, g);
+    if constexpr (OP == Op::kQuantize) {
+        // All of a thread's loads before its first store: 5.6 TB/s (147 ->
+        // 136 us for 151 M elements; the other way round it costs 8 %, 152 us
+        // against 141 one iteration at a time).
+        constexpr int kIters = kMuonTileElems / (kThreads * 8);
+        float x[kIters][8];
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+            const int e = (it * kThreads + static_cast<int>(threadIdx.x)) * 8;
+            const int n = max(0, min(8, tile.len - e));
+            load_f32(a.momentum + tile.owned + e, n == 8 && tile.aligned, n, x[it]);
+        }
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+            const int e = (it * kThreads + static_cast<int>(threadIdx.x)) * 8;
+            if ((e & ~(kMuonBlock - 1)) >= tile.len) break;       // the whole warp
+            const int n = max(0, min(8, tile.len - e));
+            store_block(a.codes + tile.owned + e, a.scales + tile.scale + e / kMuonBlock, n == 8 && tile.aligned, n, lane, x[it]);
+        }
+    } else {
+        for (int it = 0; it < kMuonTileElems / (kThreads * 8); ++it) {
+            const int e = (it * kThreads + static_cast<int>(threadIdx.x)) * 8;
+            if ((e & ~(kMuonBlock - 1)) >= tile.len) break;       // the whole warp
+            const int n = max(0, min(8, tile.len - e));
+            const bool vec = n == 8 && tile.aligned;
+            const int64_t o = tile.owned + e;
+            const int64_t block = tile.scale + e / kMuonBlock;
+            float x[8];
+            if constexpr (OP == Op::kDequantize) {
+                load_codes(a.codes + o, vec, n, a.scales[block], x);
+                store_f32(a.momentum + o, vec, n, x);
             } else {
+                if constexpr (EIGHT_BIT) load_codes(a.codes + o, vec, n, a.scales[block], x);
+                else load_f32(a.momentum + o, vec, n, x);
+                float g[8];
+                if (vec) {
+                    fold8<CAP, G>(gp, a.world_size, o, g);
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = k < n ? fold1<CAP>(gp, a.world_size, o + k) : 0.0f;
-            }
-            float u[8];
+                    for (int k = 0; k < 8; ++k) g[k] = k < n ? fold1<CAP>(gp, a.world_size, o + k) : 0.0f;
+                }
+                float u[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                g[k] = average(g[k], a);
-                x[k] = __fadd_rn(__fmul_rn(a.mu, x[k]), g[k]);
-                u[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, x[k])) : x[k];
-                if (k < n) sq += static_cast<double>(u[k]) * static_cast<double>(u[k]);
+                for (int k = 0; k < 8; ++k) {
+                    g[k] = average(g[k], a);
+                    x[k] = __fadd_rn(__fmul_rn(a.mu, x[k]), g[k]);
+                    u[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, x[k])) : x[k];
+                    if (k < n) sq += static_cast<double>(u[k]) * static_cast<double>(u[k]);
+                }
+                if constexpr (EIGHT_BIT) store_block(a.codes + o, a.scales + block, vec, n, lane, x);
+                else store_f32(a.momentum + o, vec, n, x);
+                // (the update's matrices start 8 elements apart: always aligned)
+                store_f32(a.update + tile.update + e, n == 8, n, u);
             }
-            if constexpr (EIGHT_BIT) store_block(a.codes + o, a.scales + block, vec, n, lane, x);
-            else store_f32(a.momentum + o, vec, n, x);
-            // (the update's matrices start 8 elements apart: always aligned)
-            store_f32(a.update + tile.update + e, n == 8, n, u);
         }
     }
     if constexpr (OP == Op::kMomentum) {
