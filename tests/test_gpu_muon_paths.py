@@ -10,7 +10,8 @@ import pytest
 import torch
 
 import sharded_optimizer_step_zr_b200 as zr
-from sharded_optimizer_step_zr_b200.muon import orthogonalize
+from sharded_optimizer_step_zr_b200.muon import ZrMuon, orthogonalize
+from sharded_optimizer_step_zr_b200.plan import ZrPlan
 from test_gpu_muon import DEV, Job, assert_orthogonal, quantize, randn, read_back
 
 pytestmark = pytest.mark.gpu
@@ -218,3 +219,61 @@ def test_two_optimizers_on_two_streams():
     for a, b in zip(alone, both):
         assert torch.equal(a.master, b.master) and torch.equal(a.param, b.param) and torch.equal(a.momentum, b.momentum)
         assert not b.muon.check_result()
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(36000, 60000), (60000, 36000)])
+def test_more_than_2_to_31_elements(shape):
+    """Zero but for blocks on the diagonal, one in the last corner: the
+    polynomial acts on each block alone, with the whole matrix's norm."""
+    m, n = shape
+    x = torch.zeros(m, n, dtype=torch.bfloat16, device=DEV)
+    blocks = [(0, 0, 40, 60), (17001, 20003, 130, 70), (m - 90, n - 50, 90, 50)]
+    for i, (r, c, h, w) in enumerate(blocks):
+        x[r:r + h, c:c + w] = randn(h, w, seed=i, dtype=torch.bfloat16)
+    norm = sum(x[r:r + h, c:c + w].double().square().sum() for r, c, h, w in blocks).sqrt()
+    steps = 2
+    out = orthogonalize(x, steps=steps)
+    a, b, c2 = 3.4445, -4.7750, 2.0315
+    for r, c, h, w in blocks:
+        want = x[r:r + h, c:c + w].double() / (norm + 1e-7)
+        for _ in range(steps):
+            g = want @ want.mT
+            want = a * want + (b * g + c2 * (g @ g)) @ want
+        got = out[r:r + h, c:c + w].double()
+        assert (got - want).norm() <= (2.0 ** -8 + steps * 2.0 ** -11) * want.norm()
+        out[r:r + h, c:c + w] = 0
+    assert not out.any()
+
+
+def test_master_weights_past_2_to_31_elements():
+    """A plan of more than 2^31 owned elements: the last matrix's step, its
+    8-bit codes and its scales, against the same matrix in a plan of its own."""
+    big, tail = (2 ** 17, 16640), (300, 200)
+    whole = ZrPlan([big, tail], 1, 0, zr.ZR_PARTITION_WHOLE_TENSOR, device=DEV)
+    alone = ZrPlan([tail], 1, 0, zr.ZR_PARTITION_WHOLE_TENSOR, device=DEV)
+    size, at = tail[0] * tail[1], big[0] * big[1]
+    assert at > 2 ** 31
+    got = []
+    for plan, offset in ((whole, at), (alone, 0)):
+        muon = ZrMuon(plan, lr=0.01, momentum_format="int8", ns_steps=1)
+        n = plan.owned_numel
+        grad = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+        master = torch.zeros(n, device=DEV)
+        grad[offset:offset + size] = randn(size, seed=1, dtype=torch.bfloat16)
+        master[offset:offset + size] = randn(size, seed=2)
+        codes, scales = muon.empty_momentum()
+        param = torch.zeros(plan.param_out_numel, dtype=torch.bfloat16, device=DEV)
+        muon.step([grad], master, (codes, scales), param)
+        assert not muon.check_result()
+        blocks = muon.n_scales - (size + 255) // 256
+        got.append((master[offset:offset + size].clone(), codes[offset:offset + size].clone(),
+                    scales[blocks:muon.n_scales].clone(), param[offset:offset + size].clone()))
+        if offset:
+            assert not master[:offset].any() and not codes[:offset].any() and not param[:offset].any()
+        muon.close()
+        del muon, grad, master, codes, scales, param
+    assert all(torch.equal(x, y) for x, y in zip(*got))
