@@ -352,10 +352,12 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
         uint32_t in_phase = 0;                     // parity of the next load
         const bool one = elect_one();              // the lane that issues this warp's copies
         uint32_t acc = 0;
-        for (TileWalk<NG> walk(L, pair); walk.live(); walk.next(), ++acc) {
-            const TileAt at = walk.at();
+        // One tile; the product, whether it is the last and which way X lies
+        // are compile-time choices (as branches they cost 9 % on 512 x 512).
+        auto tile = [&](const TileAt& at, auto op_, auto last_, auto tall_) -> bool {
+            constexpr int OP = decltype(op_)::value;
+            constexpr bool sym = OP != kUpdate, last = decltype(last_)::value, tall = decltype(tall_)::value;
             const IterGroup& g = L.g[at.group];
-            const bool sym = at.op != kUpdate, last = !sym && at.step + 1 == L.steps;
             const int32_t rows = sym ? g.dim : g.m, cols = sym ? g.dim : g.n;
             const int32_t row_w = at.row0 + rank * 128 + quad * 32, row = row_w + lane;
             const int32_t chunks = row_w < rows ? (min(at.bn, cols - at.col0) + 63) / 64 : 0;
@@ -367,11 +369,11 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 if (sym) tma_load_3d(hi, &maps.egram, x, row_w, at.slot, in_bar);
                 else tma_load_4d(hi, &maps.ex[at.step & 1], x, row_w, 0, at.slot, in_bar);
             };
-            const Affine k = L.k[last ? 3 : at.op];
-            const float* diag = (at.op == kPoly ? g.gram_diag : g.poly_diag) + static_cast<int64_t>(at.slot) * g.dim;
-            const bool by_row = at.op == kPoly || !g.tall, by_col = at.op == kPoly || g.tall;   // of the diagonal
+            const Affine k = L.k[last ? 3 : OP];
+            const float* diag = (OP == kPoly ? g.gram_diag : g.poly_diag) + static_cast<int64_t>(at.slot) * g.dim;
+            constexpr bool by_row = OP == kPoly || !tall, by_col = OP == kPoly || tall;         // of the diagonal
             float dr = 0.0f;
-            if (at.op != kGram && turn < chunks) {
+            if (OP != kGram && turn < chunks) {
                 bool ok = true;
                 if (one) {
                     ok = s_ready > acc || wait_slow([&] { return s_ready > acc; }, bail);
@@ -382,7 +384,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         load(turn);
                     }
                 }
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                if (!__all_sync(0xFFFFFFFFu, ok)) return false;
                 if (by_row && row < rows) dr = __ldcg(diag + row);
             }
             const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN;
@@ -399,7 +401,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                 // y: the elementwise term of a row's 64 columns, formed while
                 // the products still run
                 f32x2 y[2][16];
-                if (at.op == kGram) {
+                if constexpr (OP == kGram) {
                     if (one) store_wait_read<0>();
                 } else {
                     if (by_col) {
@@ -415,7 +417,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         ld_staged32(hi, lane, 4 * half, y[half]);
-                        if (at.op == kPoly) {
+                        if (OP == kPoly) {
                             // c A A + b A, A = D + R: acc = R R, y = b R + c (D R + R D) + (b D + c D D)
                             const float s = k.gamma * (1.0f / kNsScaleA), base = fmaf(dr, s, k.beta);
 #pragma unroll
@@ -440,7 +442,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                             constexpr float kLo = 1.0f / kNsScaleLo;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) y[half][i] = fma2(e[i], pack2(kLo, kLo), y[half][i]);
-                            if (g.tall) {
+                            if (tall) {
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2) {
                                     f32x2 d[2];
@@ -457,13 +459,20 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                         }
                     }
                 }
+                if constexpr (last && APPLY) {      // the master weights, towards L2 while the products run
+                    if (row < rows) {
+                        const float* pm = L.master + g.master_offsets[at.slot] + static_cast<int64_t>(row) * cols + c;
+                        prefetch_l2(pm);
+                        if (c + 32 < cols) prefetch_l2(pm + 32);
+                    }
+                }
                 if (ch == turn && !(ok = products())) break;
                 __syncwarp();
                 // v: 32 columns of the result from column c + 32 half on
                 auto result = [&](int half, f32x2(&v)[16]) {
                     tmem_ld32(tm + ch * 64 + half * 32, v);
                     const f32x2 alpha = pack2(k.alpha, k.alpha);
-                    if (at.op == kGram) {
+                    if (OP == kGram) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], alpha);
                     } else {
@@ -477,7 +486,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     __syncwarp();
                     if (one) mbar_arrive_cluster(free_bar + 8 * buf);
                 };
-                if (!last) {
+                if constexpr (!last) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         f32x2 v[16];
@@ -491,8 +500,8 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                                 v[i] = pack2(2 * i == lane ? 0.0f : f.x, 2 * i + 1 == lane ? 0.0f : f.y);
                             }
                             if (row < rows)
-                                (at.op == kGram ? g.gram_diag : g.poly_diag)[static_cast<int64_t>(at.slot) * g.dim + row] =
-                                    d * (at.op == kGram ? 1.0f / kNsScaleA : 1.0f / kNsScaleB);
+                                (OP == kGram ? g.gram_diag : g.poly_diag)[static_cast<int64_t>(at.slot) * g.dim + row] =
+                                    d * (OP == kGram ? 1.0f / kNsScaleA : 1.0f / kNsScaleB);
                         }
                         uint32_t w[16];
 #pragma unroll
@@ -526,14 +535,14 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     __syncwarp();
                     if (one) {
                         if (sym) {
-                            tma_store_3d(at.op == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
+                            tma_store_3d(OP == kGram ? &maps.egram : &maps.epoly, c, row_w, at.slot, hi);
                             if (mirror)
-                                tma_store_3d(at.op == kGram ? &maps.mgram : &maps.mpoly, row_w, c, at.slot, lo);
+                                tma_store_3d(OP == kGram ? &maps.mgram : &maps.mpoly, row_w, c, at.slot, lo);
                         } else {
                             tma_store_4d(&maps.ex[(at.step & 1) ^ 1], c, row_w, 0, at.slot, hi);
                         }
                         store_commit();
-                        if (at.op != kGram && ch + 2 < chunks) {
+                        if (OP != kGram && ch + 2 < chunks) {
                             store_wait_read<0>();
                             load(ch + 2);
                         }
@@ -607,24 +616,25 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     const int64_t e0 = static_cast<int64_t>(row_w) * cols + c + lane;
                     float* pm = L.master + g.master_offsets[at.slot] + e0;
                     const int64_t po = g.param_offsets[at.slot] + e0;
+                    // (two rows at a time: more spill, and the weights come from L2)
 #pragma unroll 1
-                    for (int r0 = 0; r0 < 32; r0 += 8) {
-                        float p[8][2];
+                    for (int r0 = 0; r0 < 32; r0 += 2) {
+                        float p[2][2];
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
+                        for (int r = 0; r < 2; ++r)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 if (row_w + r0 + r < rows && c + 32 * j + lane < cols)
-                                    p[r][j] = pm[static_cast<int64_t>(r0 + r) * cols + 32 * j];
+                                    p[r][j] = pm[(r0 + r) * cols + 32 * j];
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
+                        for (int r = 0; r < 2; ++r)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 if (row_w + r0 + r < rows && c + 32 * j + lane < cols) {
                                     const int cl = 32 * j + lane;
-                                    const float o = ld_shared_f32(hi + (r0 + r) * 256 + (((cl >> 2) ^ (r & 7)) << 4) + 4 * (cl & 3));
+                                    const float o = ld_shared_f32(hi + (r0 + r) * 256 + (((cl >> 2) ^ ((r0 + r) & 7)) << 4) + 4 * (cl & 3));
                                     const float q = __fsub_rn(__fmul_rn(p[r][j], L.decay), __fmul_rn(o, g.step_size));
-                                    const int64_t e = static_cast<int64_t>(r0 + r) * cols + 32 * j;
+                                    const int32_t e = (r0 + r) * cols + 32 * j;      // at most 32 rows of 2^24
                                     pm[e] = q;
                                     const uint16_t u = bf16_bits(q);
                                     if (L.n_targets == 0) L.param_out[po + e] = u;
@@ -639,9 +649,9 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     }
                 }
             }
-            if (!ok) break;
+            if (!ok) return false;
             if (turn >= chunks) {
-                if (!products()) break;
+                if (!products()) return false;
                 __syncwarp();
                 if (one) mbar_arrive_cluster(free_bar + 8 * buf);
             }
@@ -653,6 +663,21 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     red_release(g.done + at.slot, 1u);
                 }
             }
+            return true;
+        };
+        for (TileWalk<NG> walk(L, pair); walk.live(); walk.next(), ++acc) {
+            const TileAt at = walk.at();
+            using Yes = std::true_type;
+            using No = std::false_type;
+            const bool last = at.step + 1 == L.steps, tall = L.g[at.group].tall;
+            bool ok;
+            if (at.op == kGram) ok = tile(at, std::integral_constant<int, kGram>{}, No{}, No{});
+            else if (at.op == kPoly) ok = tile(at, std::integral_constant<int, kPoly>{}, No{}, No{});
+            else if (!last && !tall) ok = tile(at, std::integral_constant<int, kUpdate>{}, No{}, No{});
+            else if (!last) ok = tile(at, std::integral_constant<int, kUpdate>{}, No{}, Yes{});
+            else if (!tall) ok = tile(at, std::integral_constant<int, kUpdate>{}, Yes{}, No{});
+            else ok = tile(at, std::integral_constant<int, kUpdate>{}, Yes{}, Yes{});
+            if (!ok) break;
         }
         if (one) store_wait();
     }
