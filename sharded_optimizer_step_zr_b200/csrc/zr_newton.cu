@@ -77,6 +77,7 @@ struct IterMaps {
     CUtensorMap gram1[2], gram2[2], poly1, poly2, update1[2], update2[2];
     CUtensorMap ex[2], egram, epoly, mgram, mpoly;
 };
+static_assert(sizeof(CUtensorMap) == 128 && sizeof(IterMaps) % sizeof(CUtensorMap) == 0, "maps and nothing else");
 
 struct IterGroup {
     int32_t m, n, dim, tall;
@@ -92,13 +93,21 @@ struct IterGroup {
 };
 
 // Parameters past 4 KB cost a launch 70 us on the host, so only a single
-// group's maps are among them; those of several are in device memory.
+// group's maps are among them; those of several are in device memory, where
+// another plan's maps may have stood before: each block fences all of them
+// before its first copy.
 struct InlineMaps {
     IterMaps one;
+    __device__ __forceinline__ void fence(int32_t) const {}
     __device__ __forceinline__ const IterMaps& of(int32_t) const { return one; }
 };
 struct DeviceMaps {
     const IterMaps* all;
+    __device__ __forceinline__ void fence(int32_t n_groups) const {
+        constexpr int kMapsOfGroup = sizeof(IterMaps) / sizeof(CUtensorMap);
+        const CUtensorMap* maps = reinterpret_cast<const CUtensorMap*>(all);
+        for (int i = threadIdx.x; i < n_groups * kMapsOfGroup; i += kIterThreads) fence_tensor_map(maps + i);
+    }
     __device__ __forceinline__ const IterMaps& of(int32_t group) const { return all[group]; }
 };
 template <int NG>
@@ -256,6 +265,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    L.maps.fence(L.n_groups);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

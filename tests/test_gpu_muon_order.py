@@ -1,0 +1,39 @@
+"""What orders the matrix optimizer's work: tensor maps that replace others in
+the same memory, counters and flags between the roles of a kernel, streams and
+the lifetime of workspaces.  Each test's outputs have to be the same bits
+however the calls are arranged.
+"""
+import pytest
+import torch
+
+import sharded_optimizer_step_zr_b200 as zr
+from test_gpu_muon import DEV, Job
+
+pytestmark = pytest.mark.gpu
+
+ONE = [(200, 140), (2, 150, 260), (333, 517)]              # several shapes: their tensor maps are in the workspace
+OTHER = [(260, 330), (513, 300), (140, 150), (2, 180, 200)]
+
+
+def bind(job, workspace):
+    """The job's step on `workspace` (of any plan's size) from here on."""
+    zr.zr_muon_set_workspace(job.muon.handle, workspace, workspace.numel())
+
+
+def test_plans_take_turns_in_one_workspace():
+    """Every binding writes other tensor maps to the same addresses."""
+    alone = [Job(ONE, 1, 0, seed=1), Job(OTHER, 1, 0, seed=2)]
+    turns = [Job(ONE, 1, 0, seed=1), Job(OTHER, 1, 0, seed=2)]
+    shared = torch.empty(max(j.muon.workspace_bytes for j in turns), dtype=torch.uint8, device=DEV)
+    for j in alone + turns:
+        j.new_grads()
+    for _ in range(20):
+        for a, t in zip(alone, turns):
+            bind(t, shared)
+            t.step()
+            a.step()
+    for a, t in zip(alone, turns):
+        assert torch.equal(a.master, t.master) and torch.equal(a.momentum, t.momentum) and torch.equal(a.param, t.param)
+        assert not a.muon.check_result()
+    assert not turns[-1].muon.check_result()
+    assert torch.isfinite(alone[0].master).all()
