@@ -237,8 +237,9 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];       // the swizzle's period
     uint32_t* words = reinterpret_cast<uint32_t*>(smem_raw + kSmemBars + 8 * kBars);
     uint32_t& s_tmem = words[0];
-    volatile uint32_t &s_abort = words[1], &s_ready = words[2];     // s_ready: tiles whose operands are written
+    volatile uint32_t& s_abort = words[1];
     const uint32_t smem = smem_u32(smem_raw);
+    const uint32_t ready = smem_u32(words + 2);     // tiles whose operands are written
     const uint32_t full = smem + kSmemBars, empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, staged_in = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -247,7 +248,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
 
     if (threadIdx.x == 0) {
         s_abort = 0u;
-        s_ready = 0u;
+        words[2] = 0u;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
@@ -290,7 +291,7 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
                     if (!count_wait(g.done + at.slot, need, bail)) break;
                     fence_async_global();
                 }
-                s_ready = ++seen;
+                st_shared_release(ready, ++seen);
                 const int32_t k = at.op == kGram ? max(g.m, g.n) : g.dim;
                 const int32_t nk = (k + kBK - 1) / kBK;
                 // A box of a K-major operand is 64 contraction indices x 64 or
@@ -387,15 +388,19 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
             if (OP != kGram && turn < chunks) {
                 bool ok = true;
                 if (one) {
-                    ok = s_ready > acc || wait_slow([&] { return s_ready > acc; }, bail);
+                    // what the producer has acquired from the matrix's
+                    // counter, this lane acquires from its word, and the
+                    // barrier below passes on to the warp (a vote would not)
+                    auto written = [&] { return ld_shared_acquire(ready) > acc; };
+                    ok = written() || wait_slow(written, bail);
                     if (ok) {
-                        (void)ld_acquire(g.done + at.slot);
                         store_wait_read<0>();      // the buffer is free
                         fence_async();
                         load(turn);
                     }
                 }
                 if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+                __syncwarp();
                 if (by_row && row < rows) dr = __ldcg(diag + row);
             }
             const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN;

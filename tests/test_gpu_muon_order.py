@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import sharded_optimizer_step_zr_b200 as zr
-from test_gpu_muon import DEV, Job
+from sharded_optimizer_step_zr_b200.muon import orthogonalize
+from test_gpu_muon import DEV, Job, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,28 @@ def test_plans_take_turns_in_one_workspace():
         assert not a.muon.check_result()
     assert not turns[-1].muon.check_result()
     assert torch.isfinite(alone[0].master).all()
+
+
+@pytest.mark.parametrize("shapes", [ONE, [(777, 1025)] * 3, [(512, 512), (512, 1024), (1024, 512)]])
+def test_a_step_repeats_itself_to_the_bit(shapes):
+    """Diagonals and tiles cross from block to block many times a step; one
+    that is read before it is written shows as other bits."""
+    job = Job(shapes, 1, 0, seed=3)
+    job.new_grads()
+    start = job.master.clone()
+    job.step()
+    want = job.master.clone()
+    for _ in range(100):
+        job.momentum.zero_()
+        job.master.copy_(start)
+        job.step()
+        assert torch.equal(job.master, want)
+    assert not job.muon.check_result()
+
+
+@pytest.mark.parametrize("shape", [(6, 777, 1025), (300, 257), (128, 128), (100, 3000), (3, 1100, 900)])
+def test_a_call_repeats_itself_to_the_bit(shape):
+    x = randn(*shape, seed=5)
+    want = orthogonalize(x)
+    for _ in range(50):
+        assert torch.equal(orthogonalize(x), want)
