@@ -685,7 +685,9 @@ zr_status zr_muon_scales(const zr_muon* muon, int64_t* n_scales);
  * rounding errors and two Gram matrices (about 8 bytes per owned element and
  * 4 per element of the Gram matrices).  zr_muon_set_workspace uploads the
  * tables on `stream` and binds it, 256-byte aligned; steps that share one
- * must be ordered on the GPU.  Errors as zr_plan_set_workspace. */
+ * must be ordered on the GPU.  Errors as zr_plan_set_workspace, and
+ * ZR_ERR_UNSUPPORTED while `stream` is being captured (the tables are read
+ * from host memory); the binding that was there then stays. */
 zr_status zr_muon_workspace_bytes(const zr_muon* muon, uint64_t* bytes);
 zr_status zr_muon_set_workspace(zr_muon* muon, void* d_workspace, uint64_t bytes, zr_stream_t stream);
 /* One step.  grad_ptrs, master, param_out as zr_step's; momentum: the fp32

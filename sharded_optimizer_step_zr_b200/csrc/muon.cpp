@@ -324,9 +324,14 @@ zr_status zr_muon_set_workspace(zr_muon* u, void* d_ws, uint64_t bytes, zr_strea
     const zr_status st = current_b200(&dev);
     if (st != ZR_OK) return st;
     if (dev != u->plan->device) return ZR_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // A graph would read the host's tables again at every replay, long after
+    // they changed or went away.
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return ZR_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return ZR_ERR_UNSUPPORTED;
     u->d_workspace = nullptr;      // until all of it is in place
     char* base = static_cast<char*>(d_ws);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto up = [&](uint64_t at, const void* src, size_t n) {
         return n == 0 || cudaMemcpyAsync(base + at, src, n, cudaMemcpyHostToDevice, s) == cudaSuccess;
     };

@@ -63,3 +63,23 @@ def test_a_call_repeats_itself_to_the_bit(shape):
     want = orthogonalize(x)
     for _ in range(50):
         assert torch.equal(orthogonalize(x), want)
+
+
+def test_a_binding_is_not_captured():
+    """A replay would read the host's tables when they are gone.  The refused
+    call leaves the graph and the binding that was there as they are."""
+    a, b = Job(ONE, 1, 0, seed=4), Job(ONE, 1, 0, seed=4)
+    for j in (a, b):
+        j.new_grads()
+        j.step()
+    other = torch.empty(a.muon.workspace_bytes, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(zr.ZrError) as e:
+            bind(a, other)
+        assert e.value.status == zr.ZR_ERR_UNSUPPORTED
+        a.step()
+    for _ in range(2):
+        graph.replay()
+        b.step()
+    assert torch.equal(a.master, b.master) and torch.equal(a.momentum, b.momentum)
