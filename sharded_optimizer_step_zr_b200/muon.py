@@ -34,6 +34,16 @@ def _dtypes():
     return {torch.float32: ZR_DTYPE_F32, torch.bfloat16: ZR_DTYPE_BF16, torch.float16: ZR_DTYPE_F16}
 
 
+def _torch_stream(stream, device):
+    """A stream argument (a torch stream, or a cudaStream_t as an integer) as a torch stream of `device`."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    if stream in (0, 1):                   # the null stream, by either of its handles
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device=device)
+
+
 def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=None, stream=None):
     """Newton-Schulz orthogonalisation of x's matrices (its last two extents;
     any leading ones are a batch), as bf16.
@@ -43,8 +53,12 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     tensor of x's shape laid out alike; by default a new one.  workspace: a
     uint8 tensor of at least zr_orthogonalize_workspace_bytes on x's device,
     for calls that must not allocate; calls that share one must be ordered.
-    stream: a torch.cuda.Stream of x's device; by default that device's
-    current one."""
+    stream: a torch.cuda.Stream of x's device (or a cudaStream_t); by default
+    that device's current one.  The call is ordered by that stream alone: the
+    caller lets it wait for what writes x (and a given out or workspace), and
+    readers of the result wait for it.  What the call allocates is allocated
+    on that stream; a tensor of another stream may be dropped as soon as the
+    call has returned."""
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"x: expected a torch tensor, got {type(x).__name__}")
@@ -56,10 +70,23 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
         raise ValueError(f"x: must be on a CUDA device, is on {device}")
     if x.dim() < 2:
         raise ValueError(f"x: {x.dim()} dimensions, expected at least 2")
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, x is on {device}")
+    side = None                            # the given stream, where it is not the current one
+    if stream is not None:
+        side = _torch_stream(stream, device)
+        if side.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+            side = None
+    # A block of the current stream's memory may still be read or written by
+    # what that stream has queued, which `side` does not wait for.
+    allocating = torch.cuda.stream(side) if side is not None else _nothing
+    given = [x] + [t for t in (out, workspace) if isinstance(t, torch.Tensor)]
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=device)
-        if x.shape[-1] > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or x.shape[-2] == 1):
-            out = torch.empty(x.mT.shape, dtype=torch.bfloat16, device=device).mT
+        by_columns = x.shape[-1] > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or x.shape[-2] == 1)
+        with allocating:
+            out = torch.empty(x.mT.shape if by_columns else x.shape, dtype=torch.bfloat16, device=device)
+        if by_columns:
+            out = out.mT
     else:
         if not isinstance(out, torch.Tensor):
             raise TypeError(f"out: expected a torch tensor, got {type(out).__name__}")
@@ -93,16 +120,17 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     x_batch, x_row = strides(x, "x")
     o_batch, o_row = strides(out, "out")
     need = _workspace_bytes(batch, m, n)
-    if stream is not None and not isinstance(stream, int) and stream.device != device:
-        raise ValueError(f"stream: of {stream.device}, x is on {device}")
     with torch.cuda.device(device) if torch.cuda.current_device() != device.index else _nothing:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            if stream is not None:       # it is freed when this call returns, maybe before its work is done
-                s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-                workspace.record_stream(s)
+            with allocating:               # freed when this call returns, to the stream's own memory
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
         else:
             _require_all([(workspace, "workspace", torch.uint8, need, False)], device)
+        if side is not None:               # memory that is freed on one stream and used on another
+            for t in given:
+                t.record_stream(side)
+            if not any(t is result for t in given):
+                result.record_stream(torch.cuda.current_stream(device))
         zr_orthogonalize(x, dtype, batch, m, n, x_batch, x_row, out, o_batch, o_row, coeffs, eps, steps, workspace,
                          workspace.numel(), stream)
     return result

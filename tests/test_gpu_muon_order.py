@@ -83,3 +83,65 @@ def test_a_binding_is_not_captured():
         graph.replay()
         b.step()
     assert torch.equal(a.master, b.master) and torch.equal(a.momentum, b.momentum)
+
+
+# ---------------------------------------------------------------------------
+# streams and the lifetime of memory
+# ---------------------------------------------------------------------------
+
+BUSY = 200_000_000           # cycles: some 0.1 s in which the calls of a test are queued
+
+
+def handles(side):
+    return [side, side.cuda_stream]        # a stream is given as an object or as its handle
+
+
+@pytest.mark.parametrize("shape", [(100, 300), (300, 400)])
+def test_a_given_stream_takes_no_memory_that_the_current_one_still_reads(shape):
+    x = randn(*shape)
+    want = orthogonalize(x)
+    sizes = (2 * x.numel(), zr.zr_orthogonalize_workspace_bytes(1, *shape))
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        temporaries = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in sizes]
+        copies = [torch.zeros_like(t) for t in temporaries]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        for c, t in zip(copies, temporaries):
+            c.copy_(t)
+        del temporaries, t
+        out = orthogonalize(x, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.all(c == 7) for c in copies)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("shape", [(100, 300), (300, 400)])
+def test_tensors_may_be_dropped_while_the_given_stream_works(shape):
+    x = randn(*shape)
+    want = orthogonalize(x)
+    n = zr.zr_orthogonalize_workspace_bytes(1, *shape)
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        y, ws = x.clone(), torch.empty(n, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY)
+        out = orthogonalize(y, workspace=ws, stream=stream)
+        orthogonalize(y, stream=stream)                    # a result that nobody keeps
+        del y, ws
+        fresh = [torch.full_like(x, 5.0), torch.full((n,), 5, dtype=torch.uint8, device=DEV), torch.full_like(want, 5.0)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all(torch.all(f == 5) for f in fresh)
+
+
+def test_the_null_stream_by_its_handle():
+    x = randn(300, 400)
+    want = orthogonalize(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = [orthogonalize(x, stream=0), orthogonalize(x, stream=torch.cuda.default_stream())]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
