@@ -18,7 +18,7 @@ from . import (ZR_DTYPE_BF16, ZR_DTYPE_F16, ZR_DTYPE_F32, ZR_MOMENTUM_F32, ZR_MO
                ZR_MUON_SCALE_SPECTRAL, zr_muon_check_result, zr_muon_create, zr_muon_dequantize_momentum,
                zr_muon_destroy, zr_muon_quantize_momentum, zr_muon_scales, zr_muon_set_params,
                zr_muon_set_workspace, zr_muon_step, zr_muon_workspace_bytes, zr_orthogonalize,
-               zr_orthogonalize_workspace_bytes)
+               zr_orthogonalize_workspace_bytes, _stream)
 from .plan import _require_all
 
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -142,7 +142,13 @@ class ZrMuon:
     "int8" for codes with one fp32 scale per 256 elements; scale: "rms" (0.2
     sqrt(max(m, n))) or "spectral" (sqrt(max(1, m / n))).  The step follows
     the plan's gather targets and parameter layout; the plan is kept alive and
-    must not be closed before this object."""
+    must not be closed before this object.
+
+    The workspace is allocated, and its tables are written, on `stream` (by
+    default the current one); steps on other streams wait for that, and for
+    one another, by the caller's means.  The object may be dropped while its
+    calls still run, unless a graph captured them: it outlives the replays.
+    A stream given by its handle outlives the object."""
 
     def __init__(self, plan, lr=3e-4, momentum=0.95, weight_decay=0.1, nesterov=True, ns_steps=5,
                  ns_coeffs=MUON_COEFFS, eps=1e-7, scale="rms", momentum_format="f32", stream=None):
@@ -160,10 +166,30 @@ class ZrMuon:
         self.n_scales = zr_muon_scales(self.handle)
         self.workspace_bytes = zr_muon_workspace_bytes(self.handle)
         self.workspace = None
+        self._streams = set()                  # that both workspaces are known to be used on
+        self._plan_workspace = None
         if plan.device is not None:
-            self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=plan.device)
             with torch.cuda.device(plan.device):
+                with torch.cuda.stream(_torch_stream(stream, plan.device)) if stream is not None else _nothing:
+                    self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=plan.device)
+                self._use(stream)
                 zr_muon_set_workspace(self.handle, self.workspace, self.workspace.numel(), stream)
+
+    def _use(self, stream):
+        """Before a call on `stream`: this workspace and the plan's (which
+        holds the gather targets) are not handed out again before that stream
+        is done with them."""
+        if self.workspace is None:
+            return
+        if self._plan_workspace is not self.plan.workspace:
+            self._plan_workspace = self.plan.workspace
+            self._streams.clear()
+        handle = _stream(stream)
+        if handle not in self._streams:
+            s = _torch_stream(handle, self.plan.device)
+            for t in (self.workspace, self._plan_workspace):
+                t.record_stream(s)
+            self._streams.add(handle)
 
     def set_lr(self, lr):
         """The learning rate of the following steps."""
@@ -202,16 +228,19 @@ class ZrMuon:
             _require_all([(g, f"grads[{w}]", torch.bfloat16, n, False) for w, g in enumerate(grads)] +
                          [(master, "master", torch.float32, n, False)] + specs +
                          [(param_out, "param_out", torch.bfloat16, plan.param_out_numel, False)], plan.device)
+        self._use(stream)
         zr_muon_step(self.handle, grads, master, first, scales, param_out, stream)
 
     def quantize_momentum(self, momentum, codes, scales, stream=None):
         """zr_muon_quantize_momentum: an fp32 momentum into (codes, scales)."""
         self._check_conversion(momentum, codes, scales)
+        self._use(stream)
         zr_muon_quantize_momentum(self.handle, momentum, codes, scales, stream)
 
     def dequantize_momentum(self, codes, scales, momentum, stream=None):
         """zr_muon_dequantize_momentum: (codes, scales) into an fp32 momentum."""
         self._check_conversion(momentum, codes, scales)
+        self._use(stream)
         zr_muon_dequantize_momentum(self.handle, codes, scales, momentum, stream)
 
     def _check_conversion(self, momentum, codes, scales):
@@ -222,6 +251,7 @@ class ZrMuon:
 
     def check_result(self, stream=None):
         """True if a wait inside a step's kernels ever ran out (synchronises)."""
+        self._use(stream)
         return zr_muon_check_result(self.handle, stream)
 
     def close(self):

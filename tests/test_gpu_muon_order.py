@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import sharded_optimizer_step_zr_b200 as zr
-from sharded_optimizer_step_zr_b200.muon import orthogonalize
+from sharded_optimizer_step_zr_b200.muon import ZrMuon, orthogonalize
 from test_gpu_muon import DEV, Job, randn
 
 pytestmark = pytest.mark.gpu
@@ -92,6 +92,17 @@ def test_a_binding_is_not_captured():
 BUSY = 200_000_000           # cycles: some 0.1 s in which the calls of a test are queued
 
 
+def place(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+def assert_not_handed_out(first, end):
+    """Memory of [first, end) that a running call uses is not what the current
+    stream's next allocations get (they are not written: the call goes on)."""
+    got = [torch.empty(end - first, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    assert all(a >= end or b <= first for a, b in map(place, got))
+
+
 def handles(side):
     return [side, side.cuda_stream]        # a stream is given as an object or as its handle
 
@@ -145,3 +156,85 @@ def test_the_null_stream_by_its_handle():
         got = [orthogonalize(x, stream=0), orthogonalize(x, stream=torch.cuda.default_stream())]
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("shapes", [ONE, [(100, 60), (90, 600)]])
+def test_an_optimizer_may_be_dropped_while_its_step_runs(shapes):
+    alone = Job(shapes, 1, 0, seed=6)
+    alone.new_grads()
+    alone.step()
+    side = torch.cuda.Stream()
+    for given in handles(side) + [None]:                   # None: the side stream is the current one
+        job = Job(shapes, 1, 0, seed=6)
+        job.new_grads()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY)
+            if given is None:
+                job.step()
+        if given is not None:
+            job.step(stream=given)
+        used = place(job.muon.workspace)
+        del job.muon
+        assert_not_handed_out(*used)
+        torch.cuda.synchronize()
+        assert torch.equal(job.master, alone.master) and torch.equal(job.momentum, alone.momentum)
+
+
+def test_an_optimizer_and_its_plan_may_be_dropped_while_the_step_writes_gather_targets():
+    """The targets' addresses are read from the plan's workspace."""
+    alone, job = (Job(ONE, 2, 0, seed=9, layout=zr.ZR_PARAMS_GLOBAL) for _ in range(2))
+    targets = [[torch.zeros_like(j.param) for _ in range(2)] for j in (alone, job)]
+    for j, t in zip((alone, job), targets):
+        zr.zr_plan_set_gather_targets(j.plan.handle, t)
+        j.new_grads()
+    alone.muon.step(alone.grads, alone.master, alone.momentum, None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    job.muon.step(job.grads, job.master, job.momentum, None, stream=side)
+    used = [place(job.muon.workspace), place(job.plan.workspace)]
+    del job.muon, job.plan
+    for u in used:
+        assert_not_handed_out(*u)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*targets))
+
+
+def test_conversions_may_outlive_their_handle():
+    job = Job(ONE, 1, 0, "int8", seed=7)
+    m = job.rand(1e-2)
+    want = job.muon.empty_momentum()
+    job.muon.quantize_momentum(m, *want)
+    side = torch.cuda.Stream()
+    codes, scales = job.muon.empty_momentum()
+    back, want_back = torch.zeros_like(m), torch.zeros_like(m)
+    job.muon.dequantize_momentum(*want, want_back)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    job.muon.quantize_momentum(m, codes, scales, stream=side)
+    job.muon.dequantize_momentum(codes, scales, back, stream=side)
+    used = place(job.muon.workspace)
+    del job.muon
+    assert_not_handed_out(*used)
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1]) and torch.equal(back, want_back)
+
+
+def test_an_optimizer_made_on_a_given_stream_takes_no_memory_in_use():
+    plan = Job(ONE, 1, 0, seed=8).plan
+    n = ZrMuon(plan).workspace_bytes
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        torch.cuda.synchronize()
+        temporary = torch.full((n,), 7, dtype=torch.uint8, device=DEV)
+        copy = torch.zeros_like(temporary)
+        torch.cuda._sleep(BUSY)
+        copy.copy_(temporary)
+        del temporary
+        muon = ZrMuon(plan, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.all(copy == 7)
+        assert not muon.check_result()
