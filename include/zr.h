@@ -609,8 +609,9 @@ typedef struct {
  * may repeat), of dtype ZR_DTYPE_*; out likewise, always bf16, whose rows
  * must not overlap (out_row_stride >= n, out_batch_stride >= (m - 1) *
  * out_row_stride + n; strides of an extent of 1 are not looked at).  out may
- * be x itself with the same strides; otherwise they must not overlap.  x and
- * out need their element's alignment only.  batch, m or n of 0: nothing to
+ * be x itself with the same strides if x's elements have 16 bits; otherwise
+ * they must not overlap (refused where the two start at one address or, both
+ * without gaps, meet).  x and out need their element's alignment only.  batch, m or n of 0: nothing to
  * do, ZR_OK.
  * The workspace (zr_orthogonalize_workspace_bytes, 256-byte aligned) holds
  * fp16 copies; calls that share one must be ordered on the GPU.  Matrices
@@ -621,7 +622,7 @@ typedef struct {
  * kernel ran out and the results are not valid (not expected; the
  * alternative would be a hang).
  * Errors: ZR_ERR_INVALID_ARG (NULL, negative sizes or strides, dtype,
- * coefficients, overlapping output rows), ZR_ERR_ALIGNMENT,
+ * coefficients, overlapping output rows, out over x), ZR_ERR_ALIGNMENT,
  * ZR_ERR_NO_WORKSPACE (too small), ZR_ERR_UNSUPPORTED (an extent or the batch
  * above 2^24, the smaller extent above 2^17, more than 2e12 elements; not
  * compute capability 10.x), ZR_ERR_CUDA. */

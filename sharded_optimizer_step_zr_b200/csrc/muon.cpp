@@ -32,6 +32,19 @@ bool iteration_ok(const zr_newton_schulz& ns) {
     return zr::ns_coefficients_fit(k, ns.steps);
 }
 
+// Whether the result would certainly be written over a source that is still
+// read: the two start at one address, or are both without gaps and meet.
+// Elements of 16 bits replaced one by one are not (a matrix is read whole
+// before its result is written).
+bool overwrites(const void* x, uint64_t x_size, int64_t x_row, int64_t x_batch, const void* out, int64_t out_row,
+                int64_t out_batch, int64_t batch, int64_t m, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+    if (a == b) return x_size != 2 || x_row != out_row || x_batch != out_batch;
+    const bool dense = x_row == n && out_row == n && (batch == 1 || (x_batch == m * n && out_batch == m * n));
+    const uint64_t count = static_cast<uint64_t>(batch) * m * n;
+    return dense && a < b + 2 * count && b < a + x_size * count;
+}
+
 // A matrix of this rank, in owned order.
 struct Matrix {
     int64_t owned, global;    // first element
@@ -239,6 +252,9 @@ zr_status zr_orthogonalize(const void* x, int32_t dtype, int64_t batch, int64_t 
     if (!d_ws) return ZR_ERR_NO_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return ZR_ERR_ALIGNMENT;
     if (ws_bytes < need) return ZR_ERR_NO_WORKSPACE;
+    if (overwrites(x, dtype == ZR_DTYPE_F32 ? 4 : 2, x_row_stride, x_batch_stride, out, out_row_stride, out_batch_stride,
+                   batch, m, n))
+        return ZR_ERR_INVALID_ARG;
     int dev = 0;
     if ((st = current_b200(&dev)) != ZR_OK) return st;
 

@@ -50,7 +50,8 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
 
     x: fp32, bf16 or fp16 on a CUDA device, its rows or its columns contiguous
     (a transposed view is orthogonalised through its transpose).  out: a bf16
-    tensor of x's shape laid out alike; by default a new one.  workspace: a
+    tensor of x's shape laid out alike, which may be x itself but not overlap
+    it in another way; by default a new one.  workspace: a
     uint8 tensor of at least zr_orthogonalize_workspace_bytes on x's device,
     for calls that must not allocate; calls that share one must be ordered.
     stream: a torch.cuda.Stream of x's device (or a cudaStream_t); by default

@@ -1,0 +1,44 @@
+"""Calls of the matrix optimizer that would give wrong results and are refused
+(no GPU: a call that is let through ends at the device check instead)."""
+import pytest
+import torch
+
+import sharded_optimizer_step_zr_b200 as zr
+from test_muon_abi import P, ortho
+
+F32, BF16, F16 = zr.ZR_DTYPE_F32, zr.ZR_DTYPE_BF16, zr.ZR_DTYPE_F16
+SIZE = 2 * 8 * 16                # elements of ortho()'s default batch
+
+
+def status(**kw):
+    try:
+        ortho(**kw)
+    except zr.ZrError as e:
+        return e.status
+    return zr.ZR_OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are no device's")
+@pytest.mark.parametrize("kw,refused", [
+    (dict(dtype=F32), True),                                     # bf16 over fp32 at the same address
+    (dict(dtype=F32, batch=1), True),
+    (dict(dtype=BF16), False),                                   # in place
+    (dict(dtype=F16), False),
+    (dict(dtype=BF16, xr=20, xb=160, orow=20, ob=160), False),
+    (dict(dtype=BF16, xr=20, xb=160), True),                     # from the same address, other strides
+    (dict(dtype=BF16, xb=0), True),
+    (dict(dtype=BF16, batch=1, xb=5, ob=200), False),            # a batch of one: its stride is not looked at
+    (dict(dtype=BF16, batch=1, m=1, xr=40, orow=16), False),
+    (dict(dtype=BF16, out=P + 2), True),                         # dense, shifted
+    (dict(dtype=BF16, out=P + 2 * SIZE - 2), True),
+    (dict(dtype=BF16, out=P + 2 * SIZE), False),                 # behind it
+    (dict(dtype=BF16, out=P - 2 * SIZE), False),
+    (dict(dtype=BF16, out=P - 2 * SIZE + 2), True),
+    (dict(dtype=F32, out=P + 4 * SIZE - 2), True),
+    (dict(dtype=F32, out=P + 4 * SIZE), False),
+    (dict(dtype=BF16, xr=32, xb=256, orow=32, ob=256, out=P + 32), False),   # the halves of one buffer's rows
+])
+def test_a_result_written_over_its_source_is_refused(kw, refused):
+    got = status(**kw)
+    assert (got == zr.ZR_ERR_INVALID_ARG) == refused, got
+    assert got != zr.ZR_OK
