@@ -59,7 +59,10 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     caller lets it wait for what writes x (and a given out or workspace), and
     readers of the result wait for it.  What the call allocates is allocated
     on that stream; a tensor of another stream may be dropped as soon as the
-    call has returned."""
+    call has returned.
+
+    Not differentiable: a tensor that requires a gradient is refused where
+    gradients are recorded."""
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"x: expected a torch tensor, got {type(x).__name__}")
@@ -71,6 +74,9 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
         raise ValueError(f"x: must be on a CUDA device, is on {device}")
     if x.dim() < 2:
         raise ValueError(f"x: {x.dim()} dimensions, expected at least 2")
+    if torch.is_grad_enabled() and (x.requires_grad or getattr(out, "requires_grad", False)):
+        raise ValueError("x or out requires a gradient, which the result does not carry: detach it, or call under "
+                         "torch.no_grad()")
     if stream is not None and not isinstance(stream, int) and stream.device != device:
         raise ValueError(f"stream: of {stream.device}, x is on {device}")
     side = None                            # the given stream, where it is not the current one

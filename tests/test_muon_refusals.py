@@ -42,3 +42,26 @@ def test_a_result_written_over_its_source_is_refused(kw, refused):
     got = status(**kw)
     assert (got == zr.ZR_ERR_INVALID_ARG) == refused, got
     assert got != zr.ZR_OK
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on a CUDA device: far enough for the checks of arguments."""
+    device = torch.device("cuda", 0)
+
+
+def test_a_tensor_that_requires_a_gradient_is_refused():
+    from sharded_optimizer_step_zr_b200.muon import orthogonalize
+    x = torch.zeros(0, 4).as_subclass(OnDevice)
+    out = torch.zeros(0, 4, dtype=torch.bfloat16).as_subclass(OnDevice)
+    leaf = torch.zeros(0, 4).requires_grad_().as_subclass(OnDevice)
+    for bad in (leaf, leaf * 2):
+        assert bad.requires_grad
+        with pytest.raises(ValueError, match="gradient"):
+            orthogonalize(bad, out=out)
+        with torch.no_grad():
+            assert orthogonalize(bad, out=out) is out
+    assert orthogonalize(x, out=out) is out
+    assert orthogonalize(leaf.detach().as_subclass(OnDevice), out=out) is out
+    out.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        orthogonalize(x, out=out)
