@@ -44,7 +44,7 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(stream, device=device)
 
 
-def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=None, stream=None):
+def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=None, stream=None, status=None):
     """Newton-Schulz orthogonalisation of x's matrices (its last two extents;
     any leading ones are a batch), as bf16.
 
@@ -60,6 +60,12 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     readers of the result wait for it.  What the call allocates is allocated
     on that stream; a tensor of another stream may be dropped as soon as the
     call has returned.
+
+    status: an int32 tensor of at least one element on x's device; the call's
+    work sets its first element to 0, or to 1 if a wait inside a kernel ran
+    out, in which case the result is not valid (the first 32-bit word of a
+    given workspace says the same).  Not expected, and looked at nowhere else:
+    a call that is not given one cannot tell.
 
     Not differentiable: a tensor that requires a gradient is refused where
     gradients are recorded."""
@@ -87,7 +93,7 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     # A block of the current stream's memory may still be read or written by
     # what that stream has queued, which `side` does not wait for.
     allocating = torch.cuda.stream(side) if side is not None else _nothing
-    given = [x] + [t for t in (out, workspace) if isinstance(t, torch.Tensor)]
+    given = [x] + [t for t in (out, workspace, status) if isinstance(t, torch.Tensor)]
     if out is None:
         by_columns = x.shape[-1] > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or x.shape[-2] == 1)
         with allocating:
@@ -100,8 +106,15 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
         if out.dtype != torch.bfloat16 or out.shape != x.shape or out.device != device:
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected torch.bfloat16 "
                              f"{tuple(x.shape)} on {device}")
+    if status is not None:
+        if not isinstance(status, torch.Tensor):
+            raise TypeError(f"status: expected a torch tensor, got {type(status).__name__}")
+        _require_all([(status, "status", torch.int32, 1, False)], device)
     result = out
     if x.numel() == 0:
+        if status is not None:
+            with torch.cuda.stream(side) if side is not None else _nothing:
+                status.view(-1)[:1].zero_()
         return result
 
     def rows(t):         # columns contiguous
@@ -140,6 +153,9 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
                 result.record_stream(torch.cuda.current_stream(device))
         zr_orthogonalize(x, dtype, batch, m, n, x_batch, x_row, out, o_batch, o_row, coeffs, eps, steps, workspace,
                          workspace.numel(), stream)
+        if status is not None:
+            with torch.cuda.stream(side) if side is not None else _nothing:
+                status.view(-1)[:1].copy_(workspace[:4].view(torch.int32))
     return result
 
 

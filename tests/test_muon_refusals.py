@@ -65,3 +65,15 @@ def test_a_tensor_that_requires_a_gradient_is_refused():
     out.requires_grad_()
     with pytest.raises(ValueError, match="gradient"):
         orthogonalize(x, out=out)
+
+
+def test_a_status_of_the_wrong_kind_is_refused():
+    from sharded_optimizer_step_zr_b200.muon import orthogonalize
+    x = torch.zeros(0, 4).as_subclass(OnDevice)
+    out = torch.zeros(0, 4, dtype=torch.bfloat16).as_subclass(OnDevice)
+    with pytest.raises(TypeError, match="status"):
+        orthogonalize(x, out=out, status=0)
+    for bad in (torch.zeros(1), torch.zeros(0, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)[::2],
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="status"):            # the last one: on the host
+            orthogonalize(x, out=out, status=bad)
