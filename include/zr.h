@@ -583,10 +583,14 @@ zr_status zr_step_no_alloc(const zr_plan* plan, const void* const* grad_ptrs, fl
  * (for m > n the same polynomial from the right, on X^T X), which drives
  * every singular value towards 1 and keeps the singular vectors.  Operands
  * of the products are fp16 (scaled; X with its rounding error beside it, A
- * and B with their diagonals in fp32), sums fp32, norms fp64; the result is
- * within about 7e-4 of its norm of the exact iteration for 5 steps, before
- * its own rounding to bf16.  Elements of X_0 below 2^-46 count as zero (a
- * matrix whose norm is that far below eps).  Infinities and NaN in a matrix make that matrix's
+ * and B with their diagonals in fp32), sums fp32, norms fp64.  Off the exact
+ * iteration by, after 5 steps and before the result's own rounding to bf16:
+ * 1e-4 to 1.2e-3 of its norm for random and gradient-like matrices (7e-4 at
+ * 512 x 512, most where the extents are small and equal), up to 4e-3 with a
+ * few directions hundreds of times stronger than the rest, up to 6e-3 where
+ * all elements are of one size and the roundings do not average (a multiple of
+ * the identity).  Elements of X_0 below 2^-46 count as zero (a matrix whose
+ * norm is that far below eps).  Infinities and NaN in a matrix make that matrix's
  * result NaN or zero, as in the formula, and touch no other matrix.
  * ------------------------------------------------------------------- */
 
