@@ -618,7 +618,11 @@ typedef struct {
  * without gaps, meet).  x and out need their element's alignment only.  batch, m or n of 0: nothing to
  * do, ZR_OK.
  * The workspace (zr_orthogonalize_workspace_bytes, 256-byte aligned) holds
- * fp16 copies; calls that share one must be ordered on the GPU.  Matrices
+ * fp16 copies: 8 bytes per element of X with its n columns rounded up to 64, 4
+ * per element of a Gram matrix with its columns rounded up likewise, and some
+ * 24 bytes per matrix and its smaller extent; a narrow matrix takes many times
+ * its own size (m x 1: 512 bytes a row; the transposed view takes 8).  Calls
+ * that share one must be ordered on the GPU.  Matrices
  * whose smaller extent is above 128 (or the larger above 4096) run in a
  * cooperative kernel on up to every SM: it starts once they are free, and
  * calls on several streams follow one another.  The workspace's first
@@ -687,8 +691,8 @@ zr_status zr_muon_set_params(zr_muon* muon, const zr_muon_params* params);
 /* Scales of a ZR_MOMENTUM_INT8 state (either format may ask). */
 zr_status zr_muon_scales(const zr_muon* muon, int64_t* n_scales);
 /* Device workspace: tables, norms, and per matrix two fp16 copies with their
- * rounding errors and two Gram matrices (about 8 bytes per owned element and
- * 4 per element of the Gram matrices).  zr_muon_set_workspace uploads the
+ * rounding errors and two Gram matrices (as zr_orthogonalize's, for every
+ * matrix of the rank).  zr_muon_set_workspace uploads the
  * tables on `stream` and binds it, 256-byte aligned; steps that share one
  * must be ordered on the GPU.  Errors as zr_plan_set_workspace, and
  * ZR_ERR_UNSUPPORTED while `stream` is being captured (the tables are read

@@ -1,5 +1,6 @@
 """Calls of the matrix optimizer that would give wrong results and are refused
-(no GPU: a call that is let through ends at the device check instead)."""
+(no GPU: a call that is let through ends at the device check instead), and the
+documented sizes of workspaces."""
 import pytest
 import torch
 
@@ -77,3 +78,30 @@ def test_a_status_of_the_wrong_kind_is_refused():
                 torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(ValueError, match="status"):            # the last one: on the host
             orthogonalize(x, out=out, status=bad)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 640, 1), (1, 1, 640), (1, 4096, 3), (7, 130, 66), (24, 128, 4096), (3, 2048, 8192),
+                                   (1, 1 << 24, 1), (1 << 20, 4, 4)])
+def test_workspaces_take_the_documented_bytes(shape):
+    """8 bytes per element of X and 4 per element of a Gram matrix, columns
+    rounded up to 64; the diagonals, scales, counters and sums of squares; each
+    of twelve regions on 256 bytes."""
+    b, m, n = shape
+    g = min(m, n)
+
+    def up64(k):
+        return -(-k // 64) * 64
+    copies = 8 * b * m * up64(n) + 4 * b * g * up64(g)
+    small = 8 * b * g + 16 * b + 8 * b * -(-m // 8) * -(-n // 1024)
+    got = zr.zr_orthogonalize_workspace_bytes(b, m, n)
+    assert copies <= got <= copies + small + 12 * 256
+    if b * m * n <= 1 << 24:
+        p = zr.zr_plan_create([(b, m, n)], 1, 0, zr.ZR_PARTITION_WHOLE_TENSOR, 25 << 20)
+        u = zr.zr_muon_create(p, 3e-4, 0.95, 0.1, True, zr.ZR_MUON_SCALE_RMS, (3.4445, -4.775, 2.0315), 1e-7, 5,
+                              zr.ZR_MOMENTUM_F32)
+        tiles = b * -(-m * n // 2048)
+        got = zr.zr_muon_workspace_bytes(u)
+        maps = 16 * 128                              # of the one shape
+        assert copies <= got <= copies + 8 * b * g + 32 * b + 40 * tiles + maps + 20 * 256
+        zr.zr_muon_destroy(u)
+        zr.zr_plan_destroy(p)
