@@ -93,7 +93,7 @@ def orthogonalize(x, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, workspace=
     # A block of the current stream's memory may still be read or written by
     # what that stream has queued, which `side` does not wait for.
     allocating = torch.cuda.stream(side) if side is not None else _nothing
-    given = [x] + [t for t in (out, workspace, status) if isinstance(t, torch.Tensor)]
+    given = [x] + [t for t in (out, workspace, status) if isinstance(t, torch.Tensor)] if side is not None else ()
     if out is None:
         by_columns = x.shape[-1] > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or x.shape[-2] == 1)
         with allocating:
@@ -195,15 +195,14 @@ class ZrMuon:
             with torch.cuda.device(plan.device):
                 with torch.cuda.stream(_torch_stream(stream, plan.device)) if stream is not None else _nothing:
                     self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=plan.device)
-                self._use(stream)
-                zr_muon_set_workspace(self.handle, self.workspace, self.workspace.numel(), stream)
+                zr_muon_set_workspace(self.handle, self.workspace, self.workspace.numel(), self._use(stream))
 
     def _use(self, stream):
         """Before a call on `stream`: this workspace and the plan's (which
         holds the gather targets) are not handed out again before that stream
-        is done with them."""
+        is done with them.  Returns the stream's handle."""
         if self.workspace is None:
-            return
+            return stream
         if self._plan_workspace is not self.plan.workspace:
             self._plan_workspace = self.plan.workspace
             self._streams.clear()
@@ -213,6 +212,7 @@ class ZrMuon:
             for t in (self.workspace, self._plan_workspace):
                 t.record_stream(s)
             self._streams.add(handle)
+        return handle
 
     def set_lr(self, lr):
         """The learning rate of the following steps."""
@@ -251,20 +251,17 @@ class ZrMuon:
             _require_all([(g, f"grads[{w}]", torch.bfloat16, n, False) for w, g in enumerate(grads)] +
                          [(master, "master", torch.float32, n, False)] + specs +
                          [(param_out, "param_out", torch.bfloat16, plan.param_out_numel, False)], plan.device)
-        self._use(stream)
-        zr_muon_step(self.handle, grads, master, first, scales, param_out, stream)
+        zr_muon_step(self.handle, grads, master, first, scales, param_out, self._use(stream))
 
     def quantize_momentum(self, momentum, codes, scales, stream=None):
         """zr_muon_quantize_momentum: an fp32 momentum into (codes, scales)."""
         self._check_conversion(momentum, codes, scales)
-        self._use(stream)
-        zr_muon_quantize_momentum(self.handle, momentum, codes, scales, stream)
+        zr_muon_quantize_momentum(self.handle, momentum, codes, scales, self._use(stream))
 
     def dequantize_momentum(self, codes, scales, momentum, stream=None):
         """zr_muon_dequantize_momentum: (codes, scales) into an fp32 momentum."""
         self._check_conversion(momentum, codes, scales)
-        self._use(stream)
-        zr_muon_dequantize_momentum(self.handle, codes, scales, momentum, stream)
+        zr_muon_dequantize_momentum(self.handle, codes, scales, momentum, self._use(stream))
 
     def _check_conversion(self, momentum, codes, scales):
         import torch
@@ -274,8 +271,7 @@ class ZrMuon:
 
     def check_result(self, stream=None):
         """True if a wait inside a step's kernels ever ran out (synchronises)."""
-        self._use(stream)
-        return zr_muon_check_result(self.handle, stream)
+        return zr_muon_check_result(self.handle, self._use(stream))
 
     def close(self):
         if self.handle:
