@@ -1225,6 +1225,7 @@ int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream) {
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
                          const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream) {
     const IterMaps* maps = static_cast<const IterMaps*>(device_maps);
+    if (!apply.master && n_groups > 1) return cudaErrorInvalidValue;
     for (int32_t at = 0; at < n_groups; at += kMaxGroups) {
         const NsGroup* gs = groups + at;
         const int32_t n = std::min(kMaxGroups, n_groups - at);
@@ -1244,12 +1245,12 @@ int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps,
         Dependent<PrepLaunch> d(static_cast<unsigned>(pieces), kPrepThreads, 0, stream);
         int e = d.run(zr_ns_start_kernel, P);
         if (e != cudaSuccess) return e;
-        if (apply.master)
-            e = n == 1 ? launch_iterate<1, true>(gs, n, nullptr, steps, coeffs, apply, gave_up, stream)
-                       : launch_iterate<kMaxGroups, true>(gs, n, maps + at, steps, coeffs, apply, gave_up, stream);
+        if (!apply.master)                 // one group (zr_orthogonalize)
+            e = launch_iterate<1, false>(gs, 1, nullptr, steps, coeffs, apply, gave_up, stream);
+        else if (n == 1)
+            e = launch_iterate<1, true>(gs, n, nullptr, steps, coeffs, apply, gave_up, stream);
         else
-            e = n == 1 ? launch_iterate<1, false>(gs, n, nullptr, steps, coeffs, apply, gave_up, stream)
-                       : launch_iterate<kMaxGroups, false>(gs, n, maps + at, steps, coeffs, apply, gave_up, stream);
+            e = launch_iterate<kMaxGroups, true>(gs, n, maps + at, steps, coeffs, apply, gave_up, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -81,7 +81,7 @@ int64_t ns_partials_per_matrix(int64_t m, int64_t n);
 // and *gave_up cleared.
 int launch_ns_sumsq(const NsGroup& group, uint32_t* gave_up, void* stream);
 // The scales 1 / (norm + eps) from the partials, X_0, then `steps` iterations, then the destination.  *gave_up (device) is
-// set to 1 if a wait inside a kernel ran out.
+// set to 1 if a wait inside a kernel ran out.  Several groups only with `apply`.
 int launch_ns_iterations(const NsGroup* groups, int32_t n_groups, int32_t steps, const float coeffs[3], double eps,
                          const NsApply& apply, const void* device_maps, uint32_t* gave_up, void* stream);
 // What several groups' launches need in device memory (device_maps; 128-byte
