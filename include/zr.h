@@ -679,7 +679,9 @@ typedef struct zr_muon zr_muon;
  * tensor with elements, on any rank, has at least two extents; put other
  * tensors in a plan of their own and step them with zr_step.  *params is
  * copied.  Checked mode does not cover this step: it reads tables of its
- * own.  Errors: ZR_ERR_INVALID_ARG (NULL, a vector or scalar among the
+ * own.  zr_state_save and its kin carry zr_step's master, m and v; a momentum
+ * is the caller's to keep (owned order, as master; 8 bits as they are or
+ * through zr_muon_dequantize_momentum).  Errors: ZR_ERR_INVALID_ARG (NULL, a vector or scalar among the
  * tensors, momentum outside [0, 1), a negative or non-finite lr or
  * weight_decay, coefficients, format), ZR_ERR_UNSUPPORTED (flat partition of
  * several ranks, clipping, a shape zr_orthogonalize would refuse). */

@@ -226,12 +226,15 @@ __device__ __forceinline__ uint32_t shares_before(const IterGroup& g, const Tile
 // TMA, both halves of a row in place; a symmetric result below the diagonal
 // blocks is staged a second time transposed.
 //
-// Measured (five steps, a pass among others): 3 x 2048 x 8192 1.82 ms = 920
-// TFLOP/s of useful work and 11008 x 4096 2.93 ms = 1060, at 1.2 to 1.3 GHz
-// under the power limit (79 % of the tensor pipe's cycles; a library's fp16
-// product of the same operands sustains 1250 to 1310); 512 x 512 97 us, 15
-// products of some 11 k cycles: 3 k of copies and products, 4 k to the
-// result's visibility, 2 k to the next product's first load.
+// Measured (five steps, calls back to back, two cards): 3 x 2048 x 8192 1.76
+// to 1.85 ms = 905 to 953 TFLOP/s of useful work and 11008 x 4096 2.85 to 2.96
+// ms = 1053 to 1092, at 1.2 to 1.3 GHz under the power limit (79 % of the
+// tensor pipe's cycles; a library's fp16 product of the same operands sustains
+// 1250 to 1310).  512 x 512 95 us as a graph's replay, 15 products of some 11 k
+// cycles: 3 k of copies and products, 4 k to the result's visibility, 2 k to
+// the next product's first load.  A long thin matrix has one or two tiles of
+// A, and as many pairs contract its whole length: 128 x 4097 133 us, 128 x
+// 11008 242, 256 x 8192 189.
 template <int NG, bool APPLY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIterThreads, 1)
 zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
@@ -365,8 +368,9 @@ zr_ns_iterate_kernel(const __grid_constant__ IterLaunch<NG> L) {
         const bool one = elect_one();              // the lane that issues this warp's copies
         uint32_t acc = 0;
         // One tile; the product, whether it is the last and which way X lies
-        // are compile-time choices (as branches they cost 2 to 6 %: 6 x 777 x
-        // 1025 201 us against 194, the step of 333 x 517 107 against 101).
+        // are compile-time choices (as branches they cost 2 to 6 %; graph
+        // replays: 6 x 777 x 1025 201 us against 194, the step of 333 x 517, 1
+        // x 2000 and 640 x 1 107 against 101).
         auto tile = [&](const TileAt& at, auto op_, auto last_, auto tall_) -> bool {
             constexpr int OP = decltype(op_)::value;
             constexpr bool sym = OP != kUpdate, last = decltype(last_)::value, tall = decltype(tall_)::value;

@@ -12,9 +12,13 @@
 //          128 / C rows in the order of the CTAs),
 //   B    = b A + c A A                        (each CTA for itself),
 //   Z_c <- (a + D) Z_c + R Z_c                (local).
-// Five steps of 128 x 128: 81 us in the persistent kernel, 27 here; 100 x
-// 2000: 104 and 51; 24 of 128 x 4096: 392 and 244; 150 of 128 x 128: 153 and
-// 51.  So it is taken wherever it fits.  A step of 128 x 256 is 7.4 k cycles:
+// Five steps (graph replays) of 128 x 128: 81 us in the persistent kernel, 27
+// here; 100 x 2000: 104 and 51; 24 of 128 x 4096: 392 and 244; 150 of 128 x
+// 128: 153 and 51.  So it is taken wherever it fits.  It ends where the layout
+// does (one tile of A, 16 CTAs of 256 columns), not where the persistent
+// kernel catches up, which takes two to five times as long just past it: 129 x
+// 129 77 us, 128 x 4097 133 (128 x 4096 here: 64), 24 of 128 x 4097 405 (244),
+// 150 of 129 x 129 249 (51).  A step of 128 x 256 is 7.4 k cycles:
 // 3.5 k of products with the way into and out of tensor memory, the rest is
 // the epilogues' arithmetic; with C > 1 the exchange adds 5 to 8 k, bound by
 // the distributed shared memory.
