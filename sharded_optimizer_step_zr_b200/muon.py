@@ -201,14 +201,20 @@ class ZrMuon:
         """Before a call on `stream`: this workspace and the plan's (which
         holds the gather targets) are not handed out again before that stream
         is done with them.  Returns the stream's handle."""
+        import torch
         if self.workspace is None:
             return stream
+        device = self.plan.device
+        if stream is None and torch.cuda.current_device() != device.index:
+            return stream                      # refused by the library: nothing runs
+        if getattr(stream, "device", device) != device:
+            raise ValueError(f"stream: of {stream.device}, the plan is on {device}")
         if self._plan_workspace is not self.plan.workspace:
             self._plan_workspace = self.plan.workspace
             self._streams.clear()
         handle = _stream(stream)
         if handle not in self._streams:
-            s = _torch_stream(handle, self.plan.device)
+            s = _torch_stream(handle, device)
             for t in (self.workspace, self._plan_workspace):
                 t.record_stream(s)
             self._streams.add(handle)

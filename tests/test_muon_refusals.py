@@ -105,3 +105,38 @@ def test_workspaces_take_the_documented_bytes(shape):
         assert copies <= got <= copies + 8 * b * g + 32 * b + 40 * tiles + maps + 20 * 256
         zr.zr_muon_destroy(u)
         zr.zr_plan_destroy(p)
+
+
+class Recorder:
+    """A workspace that keeps the streams it is recorded on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, s):
+        self.streams.append(s)
+
+
+def test_a_stream_of_another_device_is_refused_and_not_kept(monkeypatch):
+    """An event on it, when the workspace is freed, would fail long after the call."""
+    from types import SimpleNamespace
+    from sharded_optimizer_step_zr_b200 import muon
+    own, other = torch.device("cuda", 0), torch.device("cuda", 1)
+    current = {"device": 1}
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current["device"])
+    monkeypatch.setattr(muon, "_stream", lambda s: 40 if s is None else s if isinstance(s, int) else s.cuda_stream)
+    monkeypatch.setattr(muon, "_torch_stream", lambda s, device: (s, device))
+    m = muon.ZrMuon.__new__(muon.ZrMuon)
+    m.handle, m._streams, m._plan_workspace = 0, set(), None
+    m.workspace, m.plan = Recorder(), SimpleNamespace(device=own, workspace=Recorder())
+    with pytest.raises(ValueError, match="stream"):
+        m._use(SimpleNamespace(device=other, cuda_stream=48))
+    assert m._use(None) is None                      # the current device is the other one
+    assert m.workspace.streams == m.plan.workspace.streams == []
+    current["device"] = 0
+    for s in (None, None, 40, SimpleNamespace(device=own, cuda_stream=56), 56, SimpleNamespace(cuda_stream=64)):
+        m._use(s)
+    assert m.workspace.streams == m.plan.workspace.streams == [(40, own), (56, own), (64, own)]
+    m.plan.workspace = Recorder()                    # bound again
+    m._use(40)
+    assert m.plan.workspace.streams == [(40, own)]
